@@ -88,7 +88,12 @@ typedef enum {
                                 that call's outputs are incomplete, the context is usable */
 } hyb_status;
 
-typedef enum { HYB_F32 = 0, HYB_BF16 = 1 } hyb_dtype;
+typedef enum {
+  HYB_F32 = 0,
+  HYB_BF16 = 1,
+  HYB_E4M3 = 2, /* 8-bit floating point, 4 exponent and 3 mantissa bits, no infinities */
+  HYB_I8 = 3    /* signed 8-bit integer, -127..127 */
+} hyb_dtype;    /* each argument says which of these it takes */
 
 /* A packed hybrid matrix; every pointer is a device pointer. */
 typedef struct {
@@ -381,6 +386,164 @@ HYB_API int hyb_spmm_skinny_nm(const hyb_matrix *A, int nk, int m, int batch,
                                const uint16_t *X, int64_t ldx, void *Y, int64_t ldy,
                                hyb_dtype ydt, void *ws, size_t ws_bytes,
                                hyb_stream_t stream);
+
+/* ---- 8-bit floating-point weights ------------------------------------------
+ * A weight held in e4m3 with one fp32 scale per 128 x 128 block, applied to
+ * activations in e4m3 with one fp32 scale per token and 128 columns:
+ *
+ *   Y[m][i] = sum_b sx[m][b] sw[i / 128][b] sum_{k in block b} xq[m][k] wq[i][k]
+ *
+ * (fp32 accumulation; the products of e4m3 values are exact).  The pages have
+ * no counterpart; it stands beside the hybrid products as the format of the
+ * layers that are kept in 8 bits.  n and k need not be multiples of 128: the
+ * last blocks are then smaller. */
+typedef struct {
+  int64_t n, k;         /* outputs, inputs */
+  const uint8_t *q;     /* [n][k] e4m3 bytes, row stride ldq */
+  int64_t ldq;          /* >= k, a multiple of 16 */
+  const float *scale;   /* [ceil(n / 128)][ceil(k / 128)], row stride lds */
+  int64_t lds;
+} hyb_fp8_matrix;
+
+/* Workspace bytes of hyb_fp8_quant (status word only). */
+HYB_API size_t hyb_fp8_quant_workspace_bytes(void);
+
+/* Quantise X [rows][cols] (xdt HYB_BF16 or HYB_F32, row stride ldx) to e4m3
+ * bytes Q (row stride ldq) and scales [ceil(rows / block_rows)]
+ * [ceil(cols / 128)] (row stride lds); block_rows is 1 (activations) or 128
+ * (weights):
+ *   a = max(largest |x| among the block's finite values, 448 * 2^-64)
+ *   scale = a / 448,  q = e4m3(sat(x * (448 / a)))
+ * each operation rounded once to fp32, the last to e4m3 (nearest even,
+ * saturating at +-448).  A NaN is stored as NaN, an infinity saturates; either
+ * sets the workspace status word (as a NaN weight does in hyb_pack).  Q 16-byte
+ * aligned and ldq a multiple of 16, as the products need them; X aligned to its
+ * element size (faster where its rows start on 16 bytes).  Bytes of Q between
+ * cols and ldq are not written. */
+HYB_API int hyb_fp8_quant(int64_t rows, int64_t cols, const void *X, int64_t ldx,
+                          hyb_dtype xdt, int block_rows, uint8_t *Q, int64_t ldq,
+                          float *scale, int64_t lds, void *ws, size_t ws_bytes,
+                          hyb_stream_t stream);
+
+/* Workspace bytes of hyb_fp8_matmul for m tokens and an n x k weight; 0 if the
+ * arguments are invalid. */
+HYB_API size_t hyb_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/* The product above for m >= 1 tokens: one decode token, a batch of them, or a
+ * prompt.  X is [m][k], row stride ldx: bf16 (xdt HYB_BF16, xs NULL), quantised
+ * inside the call exactly as hyb_fp8_quant with block_rows 1 would, or e4m3
+ * (xdt HYB_E4M3) with its scales xs [m][ceil(k / 128)] (row stride ldxs).  Y is
+ * [m][n] (ydt HYB_F32 or HYB_BF16, row stride ldy), written, not accumulated.
+ * Q and X 16-byte aligned, their row strides multiples of 16 bytes; the last
+ * row of each is read up to the next multiple of 16 bytes (what lies there is
+ * not used).  A NaN or infinity in a bf16 X sets the status word.  flags: 0 or
+ * HYB_LAUNCH_OVERLAP_PREV, with A the weight that the preceding kernel must
+ * not write.  The workspace's status word is zeroed before the first call;
+ * calls of different shapes may share a workspace that is large enough for
+ * each.  Results do not depend on the workspace or on earlier calls. */
+HYB_API int hyb_fp8_matmul(const hyb_fp8_matrix *A, int64_t m, const void *X, int64_t ldx,
+                           hyb_dtype xdt, const float *xs, int64_t ldxs, void *Y, int64_t ldy,
+                           hyb_dtype ydt, uint32_t flags, void *ws, size_t ws_bytes,
+                           hyb_stream_t stream);
+
+/* ---- 8-bit key / value cache -------------------------------------------------
+ * Keys and values of all sequences in pages of page_size tokens, 8 bits per
+ * value (HYB_E4M3 or HYB_I8) with one fp32 scale per page and head: a stored q
+ * stands for q * scale.  Sequence b's token t lies in page
+ * page_table[b][t / page_size] at place t % page_size.  Value (page, head,
+ * place, d) is at page * stride_page + head * stride_head +
+ * place * stride_token + d of k (and of v); scale (page, head) at
+ * page * kv_heads + head of k_scale (v_scale).  Strides in bytes, positive
+ * multiples of 16; any order of the axes. */
+typedef struct {
+  uint8_t *k, *v;            /* 16-byte aligned */
+  float *k_scale, *v_scale;  /* [num_pages][kv_heads] */
+  int32_t type;              /* HYB_E4M3 or HYB_I8 */
+  int32_t num_pages, kv_heads;
+  int32_t page_size;         /* 16, 32 or 64 tokens */
+  int32_t head_dim;          /* 64 or 128 */
+  int64_t stride_page, stride_head, stride_token;
+} hyb_cache;
+
+/* The sequences of one step.  lens[b] is sequence b's length in tokens AFTER
+ * this step's new tokens, the last of its length; new tokens of all sequences
+ * lie one sequence after another in the rows of K, V (hyb_cache_append) and Q,
+ * O (hyb_cache_attention): sequence b's are rows off[b] .. off[b + 1] - 1, or,
+ * with off NULL, rows b * max_new .. + max_new - 1 (every sequence has max_new
+ * of them).  An empty slot has lens[b] == 0: its rows are ignored by the
+ * append and get the empty row's result from the attention.  Device data are
+ * checked on the device: a page outside 0 .. num_pages - 1, a length below 0
+ * or above max_pages * page_size, fewer tokens than new ones (unless 0), off
+ * decreasing or outside 0 .. rows, or more than max_new new tokens, sets the
+ * status word (HYB_ERR_DEVICE_CHECK); nothing is read or written out of range
+ * (an append skips the sequence or page, an attention's rows of that sequence
+ * are unspecified). */
+typedef struct {
+  int32_t batch;              /* 1 .. 65535 */
+  int32_t max_new;            /* most new tokens of one sequence, >= 1 */
+  int64_t rows;               /* rows of K, V, Q, O (batch * max_new when off is NULL) */
+  const int32_t *lens;        /* [batch] */
+  const int32_t *off;         /* [batch + 1] or NULL */
+  const int32_t *page_table;  /* [batch][max_pages], row stride table_stride */
+  int32_t max_pages;
+  int64_t table_stride;
+} hyb_sequences;
+
+/* Workspace bytes of hyb_cache_append (status word only). */
+HYB_API size_t hyb_cache_append_workspace_bytes(void);
+
+/* Store the new tokens' keys and values (bf16, [rows][kv_heads][head_dim],
+ * row stride ldk / ldv, head stride hsk / hsv in elements, multiples of 8,
+ * 16-byte aligned) in the cache.  Per page and head that a sequence's new
+ * tokens touch, for K and V separately:
+ *   need  = the smallest 2^e, -40 <= e <= 60, with QMAX * need >= the largest
+ *           finite |x| of the new tokens there (QMAX = 448 for e4m3, 127 for
+ *           8-bit integers)
+ *   scale = max(need, the page's scale) if the page holds earlier tokens of
+ *           the sequence, else need
+ * The earlier tokens' values become round(q * (old scale / scale)), exact
+ * unless they fall below the format's steps; the new ones are
+ * round(x / scale), nearest even, saturating.  A NaN is stored as 0 and an
+ * infinity saturates; either sets the status word.  Values behind the last
+ * token stay as they were.  A page must not be written for two sequences (or
+ * by two calls) at once; pages that are only read may be shared. */
+HYB_API int hyb_cache_append(const hyb_cache *C, const hyb_sequences *S, const uint16_t *K,
+                             int64_t ldk, int64_t hsk, const uint16_t *V, int64_t ldv,
+                             int64_t hsv, void *ws, size_t ws_bytes, hyb_stream_t stream);
+
+/* Workspace bytes of hyb_cache_attention for these numbers of sequences, new
+ * tokens, pages and query heads (with any window); 0 if the arguments are
+ * invalid.  The answer depends on the current device (its SM count). */
+HYB_API size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch,
+                                                   int32_t max_new, int32_t max_pages,
+                                                   int32_t heads);
+
+/* Attention of the new tokens' queries over the cache, after their keys and
+ * values were appended:
+ *   S[i][h][t] = softmax_scale * sum_d Q[i][h][d] K[t][h / group][d]
+ *   O[i][h]    = sum_t softmax_t(S) V[t][h / group]
+ * with group = heads / kv_heads.  New token i of sequence b sits at place
+ * p = lens[b] - new + i and sees tokens t <= p; with a window W > 0 only those
+ * with t > p - W or t < sinks.  A row that sees nothing (an empty slot) gives
+ * O = 0 and lse = -infinity.
+ *   Q: bf16 [rows][heads][head_dim], row stride ldq, head stride hsq
+ *      (elements, multiples of 8, 16-byte aligned)
+ *   O: bf16 [rows][heads][head_dim], row stride ldo, head stride hso (multiples
+ *      of 8, 16-byte aligned): it is the next projection's input
+ *   lse: fp32 [rows][heads] (row stride ldl), the natural logarithm of the
+ *      softmax's sum of exponentials, or NULL
+ * heads is a multiple of kv_heads; window >= 0 (0 = none), sinks >= 0.
+ * fp32 accumulation and softmax statistics; the probabilities are rounded to
+ * 11 bits for the second product.  A cached NaN counts where a query of the
+ * sequence sees its token; tokens that none sees are not used.  Tickets and
+ * partial results live in the workspace, zeroed once before its first use and
+ * from then on used by hyb_cache_attention only (calls of different shapes may
+ * share one that is large enough for each); results are deterministic. */
+HYB_API int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16_t *Q,
+                                int64_t ldq, int64_t hsq, uint16_t *O, int64_t ldo, int64_t hso,
+                                float *lse, int64_t ldl, int32_t heads, float softmax_scale,
+                                int32_t window, int32_t sinks, void *ws, size_t ws_bytes,
+                                hyb_stream_t stream);
 
 /* ---- product without any allocation ------------------------------------ */
 

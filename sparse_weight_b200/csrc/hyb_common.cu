@@ -36,7 +36,7 @@ const char *hyb_status_string(int status) {
     case HYB_ERR_ALIGNMENT: return "pointer or leading dimension not 16-byte aligned";
     case HYB_ERR_WORKSPACE: return "workspace missing or too small";
     case HYB_ERR_CUDA: return "CUDA runtime error";
-    case HYB_ERR_DEVICE_CHECK: return "device-side data check failed (NaN weight or bad tile map)";
+    case HYB_ERR_DEVICE_CHECK: return "device-side data check failed (NaN value, bad tile map, bad sequence or page)";
     case HYB_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out (outputs incomplete)";
     default: return "unknown status";
   }

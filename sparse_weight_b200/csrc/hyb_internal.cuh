@@ -19,6 +19,7 @@ namespace hyb {
 constexpr uint32_t kStatusNaN = 1u;      // hyb_pack saw a NaN weight
 constexpr uint32_t kStatusBadMap = 2u;   // tile_map byte other than 0 / 1
 constexpr uint32_t kStatusTimeout = 4u;  // a bounded wait inside a kernel ran out
+constexpr uint32_t kStatusBadSeq = 8u;   // lengths, row offsets or page numbers out of range
 
 // Workspace header: status word, padded so that what follows is aligned.
 constexpr size_t kHeaderBytes = 256;

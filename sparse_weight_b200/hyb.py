@@ -6,6 +6,7 @@ memory and the current stream.  Function names follow the C ABI without the
 
 If ``libhyb.so`` is missing the first call raises; there is no fallback.
 """
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -28,11 +29,14 @@ HYB_ERR_TIMEOUT = -7
 
 HYB_F32 = 0
 HYB_BF16 = 1
+HYB_E4M3 = 2
+HYB_I8 = 3
 LAUNCH_OVERLAP_PREV = 1  # HYB_LAUNCH_OVERLAP_PREV
 
 STATUS_NAN = 1
 STATUS_BAD_MAP = 2
 STATUS_TIMEOUT = 4
+STATUS_BAD_SEQ = 8
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -55,6 +59,25 @@ class HybLowrank(ctypes.Structure):
                 ("V", _P), ("ldv", ctypes.c_int64)]
 
 
+class HybFp8Matrix(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("k", ctypes.c_int64), ("q", _P), ("ldq", ctypes.c_int64),
+                ("scale", _P), ("lds", ctypes.c_int64)]
+
+
+class HybCache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P),
+                ("type", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("stride_page", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("stride_token", ctypes.c_int64)]
+
+
+class HybSequences(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("lens", _P), ("off", _P), ("page_table", _P),
+                ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64)]
+
+
 class HybError(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -73,7 +96,10 @@ EXPORTS = ["hyb_packed_sizes", "hyb_pack_workspace_bytes", "hyb_pack",
            "hyb_prefill_block_shape", "hyb_spmm_prefill_blocked", "hyb_shard_bands",
            "hyb_plan_entries", "hyb_make_plan", "hyb_selftest_wait_timeout",
            "hyb_spmm_skinny_ex", "hyb_gemv_dense_ex", "hyb_packed_sizes_nm",
-           "hyb_pack_nm", "hyb_spmm_skinny_nm"]
+           "hyb_pack_nm", "hyb_spmm_skinny_nm", "hyb_fp8_quant_workspace_bytes",
+           "hyb_fp8_quant", "hyb_fp8_workspace_bytes", "hyb_fp8_matmul",
+           "hyb_cache_append_workspace_bytes", "hyb_cache_append",
+           "hyb_cache_attention_workspace_bytes", "hyb_cache_attention"]
 
 
 def lib():
@@ -161,6 +187,29 @@ def lib():
     L.hyb_spmm_skinny_nm.argtypes = [ctypes.POINTER(HybMatrix), _I, _I, _I, _P, _I64, _P,
                                      _I64, _I, _P, _SZ, _P]
     L.hyb_spmm_skinny_nm.restype = _I
+    L.hyb_fp8_quant_workspace_bytes.argtypes = []
+    L.hyb_fp8_quant_workspace_bytes.restype = _SZ
+    L.hyb_fp8_quant.argtypes = [_I64, _I64, _P, _I64, _I, _I, _P, _I64, _P, _I64, _P, _SZ, _P]
+    L.hyb_fp8_quant.restype = _I
+    L.hyb_fp8_workspace_bytes.argtypes = [_I64, _I64, _I64]
+    L.hyb_fp8_workspace_bytes.restype = _SZ
+    L.hyb_fp8_matmul.argtypes = [ctypes.POINTER(HybFp8Matrix), _I64, _P, _I64, _I, _P, _I64, _P,
+                                 _I64, _I, ctypes.c_uint32, _P, _SZ, _P]
+    L.hyb_fp8_matmul.restype = _I
+    L.hyb_cache_append_workspace_bytes.argtypes = []
+    L.hyb_cache_append_workspace_bytes.restype = _SZ
+    L.hyb_cache_append.argtypes = [ctypes.POINTER(HybCache), ctypes.POINTER(HybSequences), _P,
+                                   _I64, _I64, _P, _I64, _I64, _P, _SZ, _P]
+    L.hyb_cache_append.restype = _I
+    L.hyb_cache_attention_workspace_bytes.argtypes = [ctypes.POINTER(HybCache), ctypes.c_int32,
+                                                      ctypes.c_int32, ctypes.c_int32,
+                                                      ctypes.c_int32]
+    L.hyb_cache_attention_workspace_bytes.restype = _SZ
+    L.hyb_cache_attention.argtypes = [ctypes.POINTER(HybCache), ctypes.POINTER(HybSequences), _P,
+                                      _I64, _I64, _P, _I64, _I64, _P, _I64, ctypes.c_int32,
+                                      ctypes.c_float, ctypes.c_int32, ctypes.c_int32, _P, _SZ,
+                                      _P]
+    L.hyb_cache_attention.restype = _I
     L.hyb_status_string.argtypes = [_I]
     L.hyb_status_string.restype = ctypes.c_char_p
     _lib = L
@@ -621,3 +670,319 @@ def spmv_noalloc_check_status(stream=None) -> int:
         err.flags = flags.value
         raise err
     return flags.value
+
+
+# ---------------------------------------------------------------------------
+# 8-bit floating-point weights
+# ---------------------------------------------------------------------------
+
+def _scope(device, stream):
+    """Make ``device`` current and ``stream`` (or the device's current stream)
+    the one that new tensors belong to; returns (stream handle, context).
+    Outputs and workspaces made inside a call are then allocated in the order
+    of the stream that uses them."""
+    if stream is None:
+        if device.index is None or device.index == torch.cuda.current_device():
+            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), _NO_SCOPE
+        return (ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream),
+                torch.cuda.device(device))
+    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _on_device(fn, device, *tensors):
+    """Every tensor lives on the CUDA device of the first."""
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: tensors must live on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
+
+
+def _want(fn, ok, what):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+@dataclass
+class Fp8Matrix:
+    """An e4m3 weight with one fp32 scale per 128 x 128 block, on the device."""
+    n: int
+    k: int
+    q: torch.Tensor      # float8_e4m3fn [n][k], rows a multiple of 16 bytes apart
+    scale: torch.Tensor  # fp32 [ceil(n / 128)][ceil(k / 128)]
+
+    def __post_init__(self):
+        f = "Fp8Matrix"
+        _want(f, self.q.dtype in (torch.float8_e4m3fn, torch.uint8), "q must be float8_e4m3fn")
+        _want(f, self.scale.dtype == torch.float32, "scale must be fp32")
+        _want(f, tuple(self.q.shape) == (self.n, self.k), "q must be [n][k]")
+        _want(f, tuple(self.scale.shape) == (-(-self.n // 128), -(-self.k // 128)),
+              "scale must be [ceil(n / 128)][ceil(k / 128)]")
+        _want(f, (self.k == 1 or self.q.stride(1) == 1)
+              and (self.scale.shape[1] == 1 or self.scale.stride(1) == 1),
+              "rows of q and scale must be contiguous")
+
+    def struct(self) -> HybFp8Matrix:
+        # a single row's or column's stride says nothing: at least the row's length
+        kb = self.scale.shape[1]
+        return HybFp8Matrix(self.n, self.k, self.q.data_ptr(),
+                            self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
+                            self.scale.data_ptr(), max(self.scale.stride(0), kb))
+
+    def nbytes(self) -> int:
+        """Bytes the product streams (values + scales)."""
+        return self.n * self.k + 4 * self.scale.numel()
+
+
+def fp8_quant_workspace_bytes() -> int:
+    return int(lib().hyb_fp8_quant_workspace_bytes())
+
+
+def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, stream=None):
+    """hyb_fp8_quant: bf16 or fp32 X [rows][cols] -> (q float8_e4m3fn [rows][cols],
+    scale fp32 [ceil(rows / block_rows)][ceil(cols / 128)]).  The rows of q lie a
+    multiple of 16 bytes apart, as the products need them."""
+    _want("quant_fp8", X.dim() == 2 and X.shape[0] > 0 and X.shape[1] > 0, "X must be [rows][cols]")
+    _want("quant_fp8", X.dtype in (torch.bfloat16, torch.float32), "X must be bf16 or fp32")
+    _want("quant_fp8", X.shape[1] == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    rows, cols = X.shape
+    dev = X.device
+    _on_device("quant_fp8", dev, ws)
+    handle, scope = _scope(dev, stream)
+    with scope:
+        ld = -(-cols // 16) * 16
+        q = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=dev)
+        if ld != cols:
+            q = q[:, :cols]
+        cb = -(-cols // 128)
+        s = torch.empty(-(-rows // block_rows) if block_rows > 0 else 1, cb, dtype=torch.float32,
+                        device=dev)
+        if ws is None:
+            ws = new_workspace(fp8_quant_workspace_bytes(), dev)
+        f32 = X.dtype == torch.float32
+        _check("hyb_fp8_quant", lib().hyb_fp8_quant(
+            rows, cols, X.data_ptr(), max(X.stride(0), cols),
+            HYB_F32 if f32 else HYB_BF16, block_rows, q.data_ptr(), ld, s.data_ptr(), cb,
+            ws.data_ptr(), ws.numel(), handle))
+    return q, s
+
+
+def pack_fp8(W: torch.Tensor, ws: torch.Tensor = None, stream=None,
+             check: bool = True) -> Fp8Matrix:
+    """A bf16 or fp32 weight W [n][k] as an Fp8Matrix (hyb_fp8_quant with
+    128 x 128 blocks).  With ``check`` the call synchronises and raises HybError
+    on a NaN or infinite weight."""
+    if ws is None:
+        with _scope(W.device, stream)[1]:
+            ws = new_workspace(fp8_quant_workspace_bytes(), W.device)
+    q, s = quant_fp8(W, 128, ws, stream)
+    if check:
+        check_status(ws, stream)
+    return Fp8Matrix(W.shape[0], W.shape[1], q, s)
+
+
+def fp8_workspace_bytes(m: int, n: int, k: int) -> int:
+    nbytes = int(lib().hyb_fp8_workspace_bytes(m, n, k))
+    if nbytes == 0:
+        raise HybError("hyb_fp8_workspace_bytes", HYB_ERR_INVALID_ARG)
+    return nbytes
+
+
+def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.Tensor = None,
+               ydt: int = HYB_F32, ws: torch.Tensor = None, stream=None,
+               flags: int = 0) -> torch.Tensor:
+    """hyb_fp8_matmul: Y[m][n] = W X for an e4m3 weight and any number of tokens.
+    X is bf16 [m][k] (or [k]), quantised inside the call, or float8_e4m3fn with
+    its scales xs (quant_fp8).  flags as for spmm_skinny."""
+    f = "matmul_fp8"
+    if X.dim() == 1:
+        X = X.view(1, -1)
+    m = X.shape[0]
+    _want(f, X.dim() == 2 and X.shape[1] == A.k and m > 0, "X must be [m][k]")
+    _want(f, A.k == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    if xs is None:
+        _want(f, X.dtype == torch.bfloat16, "X must be bf16, or e4m3 with xs")
+    else:
+        _want(f, X.dtype == torch.float8_e4m3fn, "X with xs must be float8_e4m3fn")
+        _want(f, xs.dtype == torch.float32 and tuple(xs.shape) == (m, A.scale.shape[1])
+              and (xs.shape[1] == 1 or xs.stride(1) == 1), "xs must be fp32 [m][ceil(k / 128)]")
+    dev = X.device
+    _on_device(f, dev, A.q, A.scale, xs, Y, ws)
+    handle, scope = _scope(dev, stream)
+    with scope:
+        if Y is None:
+            Y = torch.empty(m, A.n, dtype=torch.float32 if ydt == HYB_F32 else torch.bfloat16,
+                            device=dev)
+        else:
+            _want(f, tuple(Y.shape) == (m, A.n) and (A.n == 1 or Y.stride(1) == 1)
+                  and Y.dtype == (torch.float32 if ydt == HYB_F32 else torch.bfloat16),
+                  "Y must be [m][n] in ydt")
+        if ws is None:
+            ws = new_workspace(fp8_workspace_bytes(m, A.n, A.k), dev)
+        s = A.struct()
+        _check("hyb_fp8_matmul", lib().hyb_fp8_matmul(
+            ctypes.byref(s), m, X.data_ptr(), X.stride(0) if m > 1 else -(-A.k // 16) * 16,
+            HYB_BF16 if xs is None else HYB_E4M3, None if xs is None else xs.data_ptr(),
+            0 if xs is None else max(xs.stride(0), xs.shape[1]), Y.data_ptr(),
+            Y.stride(0) if m > 1 else A.n, ydt, flags, ws.data_ptr(), ws.numel(), handle))
+    return Y
+
+
+# ---------------------------------------------------------------------------
+# 8-bit key / value cache
+# ---------------------------------------------------------------------------
+
+@dataclass
+class Cache:
+    """Keys and values in pages of 8-bit values with one scale per page and
+    head (hyb_cache).  k, v: [num_pages][kv_heads][page_size][head_dim], any
+    strides (multiples of 16) with head_dim contiguous."""
+    k: torch.Tensor        # float8_e4m3fn or int8
+    v: torch.Tensor
+    k_scale: torch.Tensor  # fp32 [num_pages][kv_heads]
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        f = "Cache"
+        _want(f, self.k.dtype in (torch.float8_e4m3fn, torch.int8) and self.v.dtype == self.k.dtype,
+              "k and v must both be float8_e4m3fn or both int8")
+        _want(f, self.k.dim() == 4 and self.v.shape == self.k.shape
+              and self.v.stride() == self.k.stride() and self.k.stride(3) == 1,
+              "k and v must be [pages][heads][tokens][dim] of the same strides, dim contiguous")
+        _want(f, all(s.dtype == torch.float32 and s.shape == self.k.shape[:2] and s.is_contiguous()
+                     for s in (self.k_scale, self.v_scale)),
+              "scales must be contiguous fp32 [pages][heads]")
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    def struct(self) -> HybCache:
+        pages, heads, size, dim = self.k.shape
+        sp, sh, st, _ = self.k.stride()
+        return HybCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                        self.v_scale.data_ptr(),
+                        HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages, heads, size,
+                        dim, sp, sh, st)
+
+
+def new_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
+              dtype=torch.float8_e4m3fn, device="cuda") -> Cache:
+    """An empty cache (zeros)."""
+    kv = [torch.zeros(num_pages, kv_heads, page_size, head_dim, dtype=torch.uint8,
+                      device=device).view(dtype) for _ in range(2)]
+    sc = [torch.zeros(num_pages, kv_heads, device=device) for _ in range(2)]
+    return Cache(kv[0], kv[1], sc[0], sc[1])
+
+
+def _sequences(f, rows, page_table, lens, off, max_new):
+    _want(f, page_table.dim() == 2 and page_table.dtype == torch.int32
+          and (page_table.shape[1] == 1 or page_table.stride(1) == 1),
+          "page_table must be int32 [batch][pages]")
+    batch, pages = page_table.shape
+    _want(f, lens.dtype == torch.int32 and tuple(lens.shape) == (batch,) and lens.is_contiguous(),
+          "lens must be int32 [batch]")
+    if off is None:
+        if max_new is None and batch and rows % batch == 0:
+            max_new = rows // batch
+        _want(f, max_new is not None and rows == batch * max_new,
+              "without off every sequence has max_new rows")
+    else:
+        _want(f, off.dtype == torch.int32 and tuple(off.shape) == (batch + 1,)
+              and off.is_contiguous(), "off must be int32 [batch + 1]")
+        _want(f, max_new is not None, "off needs max_new")
+    return HybSequences(batch, max_new, rows, lens.data_ptr(),
+                        None if off is None else off.data_ptr(), page_table.data_ptr(), pages,
+                        max(page_table.stride(0), pages))
+
+
+def _heads(f, x, heads, dim, what):
+    """(row stride, head stride) of bf16 rows [rows][heads][dim]."""
+    _want(f, x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == dim
+          and (heads is None or x.shape[1] == heads) and x.stride(2) == 1,
+          f"{what} must be bf16 [rows][heads][head_dim] with head_dim contiguous")
+    return (x.stride(0) if x.shape[0] > 1 else max(dim, x.shape[1] * dim),
+            x.stride(1) if x.shape[1] > 1 else dim)
+
+
+def cache_append_workspace_bytes() -> int:
+    return int(lib().hyb_cache_append_workspace_bytes())
+
+
+def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.Tensor,
+                 lens: torch.Tensor, off: torch.Tensor = None, max_new: int = None,
+                 ws: torch.Tensor = None, stream=None) -> None:
+    """hyb_cache_append: store new keys and values (bf16 [rows][kv_heads][head_dim])
+    as the last tokens of sequences whose lengths are ``lens`` with them.  off
+    [batch + 1]: the sequences' rows (None: max_new rows each)."""
+    f = "cache_append"
+    heads, dim = C.k.shape[1], C.k.shape[3]
+    ldk, hsk = _heads(f, K, heads, dim, "K")
+    ldv, hsv = _heads(f, V, heads, dim, "V")
+    _want(f, K.shape[0] == V.shape[0], "K and V must have the same rows")
+    dev = C.k.device
+    _on_device(f, dev, C.v, C.k_scale, C.v_scale, K, V, page_table, lens, off, ws)
+    seq = _sequences(f, K.shape[0], page_table, lens, off, max_new)
+    if K.shape[0] == 0:
+        return
+    handle, scope = _scope(dev, stream)
+    with scope:
+        if ws is None:
+            ws = new_workspace(cache_append_workspace_bytes(), dev)
+        c = C.struct()
+        _check("hyb_cache_append", lib().hyb_cache_append(
+            ctypes.byref(c), ctypes.byref(seq), K.data_ptr(), ldk, hsk, V.data_ptr(), ldv, hsv,
+            ws.data_ptr(), ws.numel(), handle))
+
+
+def cache_attention_workspace_bytes(C: Cache, batch: int, heads: int, max_new: int,
+                                    max_len: int) -> int:
+    """For sequences of up to max_len tokens (the page table's width times the
+    page size) and max_new new ones."""
+    c = C.struct()
+    n = int(lib().hyb_cache_attention_workspace_bytes(
+        ctypes.byref(c), batch, max_new, -(-max_len // C.page_size), heads))
+    if n == 0:
+        raise HybError("hyb_cache_attention_workspace_bytes", HYB_ERR_INVALID_ARG)
+    return n
+
+
+def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                    off: torch.Tensor = None, max_new: int = None, scale: float = None,
+                    window: int = 0, sinks: int = 0, out: torch.Tensor = None,
+                    return_lse: bool = False, ws: torch.Tensor = None, stream=None):
+    """hyb_cache_attention: the new tokens' queries (bf16 [rows][heads][head_dim])
+    over the cache; causal, with a sliding window and first tokens that stay
+    visible (sinks) where window > 0.  scale defaults to 1 / sqrt(head_dim).
+    Returns O (bf16, as Q), with return_lse also the fp32 log-sum-exp
+    [rows][heads]."""
+    f = "cache_attention"
+    dim = C.k.shape[3]
+    ldq, hsq = _heads(f, Q, None, dim, "Q")
+    rows, heads = Q.shape[0], Q.shape[1]
+    dev = C.k.device
+    _on_device(f, dev, C.v, C.k_scale, C.v_scale, Q, page_table, lens, off, out, ws)
+    seq = _sequences(f, rows, page_table, lens, off, max_new)
+    handle, scope = _scope(dev, stream)
+    with scope:
+        if out is None:
+            out = torch.empty(rows, heads, dim, dtype=torch.bfloat16, device=dev)
+            ldo, hso = heads * dim, dim
+        else:
+            _want(f, out.shape == Q.shape, "out must have Q's shape")
+            ldo, hso = _heads(f, out, heads, dim, "out")
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev) if return_lse else None
+        if rows:
+            if ws is None:
+                ws = new_workspace(cache_attention_workspace_bytes(
+                    C, seq.batch, heads, seq.max_new, seq.max_pages * C.page_size), dev)
+            c = C.struct()
+            _check("hyb_cache_attention", lib().hyb_cache_attention(
+                ctypes.byref(c), ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo,
+                hso, lse.data_ptr() if return_lse else None, heads, heads,
+                dim ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),
+                handle))
+    return (out, lse) if return_lse else out
