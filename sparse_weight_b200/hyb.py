@@ -676,20 +676,22 @@ def spmv_noalloc_check_status(stream=None) -> int:
 # 8-bit floating-point weights
 # ---------------------------------------------------------------------------
 
+_NO_SCOPE = contextlib.nullcontext()
+# the current stream's handle without a Stream object around it (3 us less per call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _scope(device, stream):
     """Make ``device`` current and ``stream`` (or the device's current stream)
     the one that new tensors belong to; returns (stream handle, context).
     Outputs and workspaces made inside a call are then allocated in the order
     of the stream that uses them."""
-    if stream is None:
-        if device.index is None or device.index == torch.cuda.current_device():
-            return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), _NO_SCOPE
-        return (ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream),
-                torch.cuda.device(device))
-    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
-
-
-_NO_SCOPE = contextlib.nullcontext()
+    if stream is not None:
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        return _raw_stream(index), _NO_SCOPE
+    return _raw_stream(index), torch.cuda.device(device)
 
 
 def _on_device(fn, device, *tensors):
@@ -706,7 +708,7 @@ def _want(fn, ok, what):
         raise ValueError(f"{fn}: {what}")
 
 
-@dataclass
+@dataclass(frozen=True)
 class Fp8Matrix:
     """An e4m3 weight with one fp32 scale per 128 x 128 block, on the device."""
     n: int
@@ -724,13 +726,16 @@ class Fp8Matrix:
         _want(f, (self.k == 1 or self.q.stride(1) == 1)
               and (self.scale.shape[1] == 1 or self.scale.stride(1) == 1),
               "rows of q and scale must be contiguous")
+        # the C struct, made once: the fields cannot be assigned again
+        # (a single row's stride says nothing: at least the row's length)
+        kb = self.scale.shape[1]
+        object.__setattr__(self, "_struct", HybFp8Matrix(
+            self.n, self.k, self.q.data_ptr(),
+            self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
+            self.scale.data_ptr(), max(self.scale.stride(0), kb)))
 
     def struct(self) -> HybFp8Matrix:
-        # a single row's or column's stride says nothing: at least the row's length
-        kb = self.scale.shape[1]
-        return HybFp8Matrix(self.n, self.k, self.q.data_ptr(),
-                            self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
-                            self.scale.data_ptr(), max(self.scale.stride(0), kb))
+        return self._struct
 
     def nbytes(self) -> int:
         """Bytes the product streams (values + scales)."""
@@ -745,29 +750,35 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
     """hyb_fp8_quant: bf16 or fp32 X [rows][cols] -> (q float8_e4m3fn [rows][cols],
     scale fp32 [ceil(rows / block_rows)][ceil(cols / 128)]).  The rows of q lie a
     multiple of 16 bytes apart, as the products need them."""
-    _want("quant_fp8", X.dim() == 2 and X.shape[0] > 0 and X.shape[1] > 0, "X must be [rows][cols]")
-    _want("quant_fp8", X.dtype in (torch.bfloat16, torch.float32), "X must be bf16 or fp32")
-    _want("quant_fp8", X.shape[1] == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    f = "quant_fp8"
+    xdt = _QUANT_TYPES.get(X.dtype)
+    if xdt is None:
+        raise ValueError(f"{f}: X must be bf16 or fp32")
+    _want(f, X.dim() == 2, "X must be [rows][cols]")
     rows, cols = X.shape
+    ldx = X.stride(0)
+    _want(f, rows > 0 and cols > 0, "X must not be empty")
+    _want(f, cols == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    _want(f, block_rows in (1, 128), "block_rows must be 1 or 128")
     dev = X.device
-    _on_device("quant_fp8", dev, ws)
+    _on_device(f, dev, ws)
     handle, scope = _scope(dev, stream)
+    ld, cb = -(-cols // 16) * 16, -(-cols // 128)
     with scope:
-        ld = -(-cols // 16) * 16
-        q = torch.empty(rows, ld, dtype=torch.float8_e4m3fn, device=dev)
+        q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=dev)
         if ld != cols:
             q = q[:, :cols]
-        cb = -(-cols // 128)
-        s = torch.empty(-(-rows // block_rows) if block_rows > 0 else 1, cb, dtype=torch.float32,
-                        device=dev)
+        s = torch.empty((-(-rows // block_rows), cb), dtype=torch.float32, device=dev)
         if ws is None:
             ws = new_workspace(fp8_quant_workspace_bytes(), dev)
-        f32 = X.dtype == torch.float32
-        _check("hyb_fp8_quant", lib().hyb_fp8_quant(
-            rows, cols, X.data_ptr(), max(X.stride(0), cols),
-            HYB_F32 if f32 else HYB_BF16, block_rows, q.data_ptr(), ld, s.data_ptr(), cb,
-            ws.data_ptr(), ws.numel(), handle))
+        rc = lib().hyb_fp8_quant(rows, cols, X.data_ptr(), ldx if ldx > cols else cols, xdt,
+                                 block_rows, q.data_ptr(), ld, s.data_ptr(), cb, ws.data_ptr(),
+                                 ws.numel(), handle)
+    _check("hyb_fp8_quant", rc)
     return q, s
+
+
+_QUANT_TYPES = {torch.bfloat16: HYB_BF16, torch.float32: HYB_F32}
 
 
 def pack_fp8(W: torch.Tensor, ws: torch.Tensor = None, stream=None,
@@ -800,42 +811,48 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
     f = "matmul_fp8"
     if X.dim() == 1:
         X = X.view(1, -1)
+    n, k = A.n, A.k
+    _want(f, X.dim() == 2 and X.shape[1] == k and X.shape[0] > 0, "X must be [m][k]")
     m = X.shape[0]
-    _want(f, X.dim() == 2 and X.shape[1] == A.k and m > 0, "X must be [m][k]")
-    _want(f, A.k == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    ldx = X.stride(0)
+    _want(f, k == 1 or X.stride(1) == 1, "rows of X must be contiguous")
     if xs is None:
         _want(f, X.dtype == torch.bfloat16, "X must be bf16, or e4m3 with xs")
     else:
         _want(f, X.dtype == torch.float8_e4m3fn, "X with xs must be float8_e4m3fn")
-        _want(f, xs.dtype == torch.float32 and tuple(xs.shape) == (m, A.scale.shape[1])
+        _want(f, xs.dtype == torch.float32 and xs.shape == (m, A.scale.shape[1])
               and (xs.shape[1] == 1 or xs.stride(1) == 1), "xs must be fp32 [m][ceil(k / 128)]")
+    ytype = _OUT_TYPES.get(ydt)
+    _want(f, ytype is not None, "ydt must be HYB_F32 or HYB_BF16")
+    if Y is not None:
+        _want(f, Y.shape == (m, n) and (n == 1 or Y.stride(1) == 1) and Y.dtype == ytype,
+              "Y must be [m][n] in ydt")
     dev = X.device
     _on_device(f, dev, A.q, A.scale, xs, Y, ws)
     handle, scope = _scope(dev, stream)
     with scope:
         if Y is None:
-            Y = torch.empty(m, A.n, dtype=torch.float32 if ydt == HYB_F32 else torch.bfloat16,
-                            device=dev)
-        else:
-            _want(f, tuple(Y.shape) == (m, A.n) and (A.n == 1 or Y.stride(1) == 1)
-                  and Y.dtype == (torch.float32 if ydt == HYB_F32 else torch.bfloat16),
-                  "Y must be [m][n] in ydt")
+            Y = torch.empty((m, n), dtype=ytype, device=dev)
         if ws is None:
-            ws = new_workspace(fp8_workspace_bytes(m, A.n, A.k), dev)
-        s = A.struct()
-        _check("hyb_fp8_matmul", lib().hyb_fp8_matmul(
-            ctypes.byref(s), m, X.data_ptr(), X.stride(0) if m > 1 else -(-A.k // 16) * 16,
+            ws = new_workspace(fp8_workspace_bytes(m, n, k), dev)
+        # a single row's stride says nothing
+        rc = lib().hyb_fp8_matmul(
+            ctypes.byref(A._struct), m, X.data_ptr(), ldx if m > 1 else -(-k // 16) * 16,
             HYB_BF16 if xs is None else HYB_E4M3, None if xs is None else xs.data_ptr(),
             0 if xs is None else max(xs.stride(0), xs.shape[1]), Y.data_ptr(),
-            Y.stride(0) if m > 1 else A.n, ydt, flags, ws.data_ptr(), ws.numel(), handle))
+            Y.stride(0) if m > 1 else n, ydt, flags, ws.data_ptr(), ws.numel(), handle)
+    _check("hyb_fp8_matmul", rc)
     return Y
+
+
+_OUT_TYPES = {HYB_F32: torch.float32, HYB_BF16: torch.bfloat16}
 
 
 # ---------------------------------------------------------------------------
 # 8-bit key / value cache
 # ---------------------------------------------------------------------------
 
-@dataclass
+@dataclass(frozen=True)
 class Cache:
     """Keys and values in pages of 8-bit values with one scale per page and
     head (hyb_cache).  k, v: [num_pages][kv_heads][page_size][head_dim], any
@@ -855,18 +872,22 @@ class Cache:
         _want(f, all(s.dtype == torch.float32 and s.shape == self.k.shape[:2] and s.is_contiguous()
                      for s in (self.k_scale, self.v_scale)),
               "scales must be contiguous fp32 [pages][heads]")
+        _want(f, all(x.device == self.k.device for x in (self.v, self.k_scale, self.v_scale)),
+              "all tensors must live on one device")
+        # the C struct, made once: the fields cannot be assigned again
+        pages, heads, size, dim = self.k.shape
+        sp, sh, st, _ = self.k.stride()
+        object.__setattr__(self, "_struct", HybCache(
+            self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+            self.v_scale.data_ptr(), HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages,
+            heads, size, dim, sp, sh, st))
 
     @property
     def page_size(self) -> int:
         return self.k.shape[2]
 
     def struct(self) -> HybCache:
-        pages, heads, size, dim = self.k.shape
-        sp, sh, st, _ = self.k.stride()
-        return HybCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-                        self.v_scale.data_ptr(),
-                        HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages, heads, size,
-                        dim, sp, sh, st)
+        return self._struct
 
 
 def new_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
@@ -879,33 +900,36 @@ def new_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
 
 
 def _sequences(f, rows, page_table, lens, off, max_new):
-    _want(f, page_table.dim() == 2 and page_table.dtype == torch.int32
-          and (page_table.shape[1] == 1 or page_table.stride(1) == 1),
-          "page_table must be int32 [batch][pages]")
+    _want(f, page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table must be int32 "
+          "[batch][pages]")
     batch, pages = page_table.shape
-    _want(f, lens.dtype == torch.int32 and tuple(lens.shape) == (batch,) and lens.is_contiguous(),
+    stride, one = page_table.stride()
+    _want(f, pages == 1 or one == 1, "rows of page_table must be contiguous")
+    _want(f, lens.dtype == torch.int32 and lens.shape == (batch,) and lens.is_contiguous(),
           "lens must be int32 [batch]")
     if off is None:
         if max_new is None and batch and rows % batch == 0:
             max_new = rows // batch
         _want(f, max_new is not None and rows == batch * max_new,
               "without off every sequence has max_new rows")
+        at = None
     else:
-        _want(f, off.dtype == torch.int32 and tuple(off.shape) == (batch + 1,)
-              and off.is_contiguous(), "off must be int32 [batch + 1]")
+        _want(f, off.dtype == torch.int32 and off.shape == (batch + 1,) and off.is_contiguous(),
+              "off must be int32 [batch + 1]")
         _want(f, max_new is not None, "off needs max_new")
-    return HybSequences(batch, max_new, rows, lens.data_ptr(),
-                        None if off is None else off.data_ptr(), page_table.data_ptr(), pages,
-                        max(page_table.stride(0), pages))
+        at = off.data_ptr()
+    return HybSequences(batch, max_new, rows, lens.data_ptr(), at, page_table.data_ptr(), pages,
+                        stride if stride > pages else pages)
 
 
 def _heads(f, x, heads, dim, what):
-    """(row stride, head stride) of bf16 rows [rows][heads][dim]."""
-    _want(f, x.dtype == torch.bfloat16 and x.dim() == 3 and x.shape[2] == dim
-          and (heads is None or x.shape[1] == heads) and x.stride(2) == 1,
-          f"{what} must be bf16 [rows][heads][head_dim] with head_dim contiguous")
-    return (x.stride(0) if x.shape[0] > 1 else max(dim, x.shape[1] * dim),
-            x.stride(1) if x.shape[1] > 1 else dim)
+    """(rows, heads, row stride, head stride) of bf16 rows [rows][heads][dim]."""
+    if x.dtype == torch.bfloat16 and x.dim() == 3:
+        rows, h, d = x.shape
+        ld, hs, one = x.stride()
+        if d == dim and (heads is None or h == heads) and one == 1:
+            return rows, h, ld if rows > 1 else max(dim, h * dim), hs if h > 1 else dim
+    raise ValueError(f"{f}: {what} must be bf16 [rows][heads][head_dim] with head_dim contiguous")
 
 
 def cache_append_workspace_bytes() -> int:
@@ -919,23 +943,22 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
     as the last tokens of sequences whose lengths are ``lens`` with them.  off
     [batch + 1]: the sequences' rows (None: max_new rows each)."""
     f = "cache_append"
-    heads, dim = C.k.shape[1], C.k.shape[3]
-    ldk, hsk = _heads(f, K, heads, dim, "K")
-    ldv, hsv = _heads(f, V, heads, dim, "V")
-    _want(f, K.shape[0] == V.shape[0], "K and V must have the same rows")
+    c = C._struct
+    rows, _, ldk, hsk = _heads(f, K, c.kv_heads, c.head_dim, "K")
+    rows_v, _, ldv, hsv = _heads(f, V, c.kv_heads, c.head_dim, "V")
+    _want(f, rows == rows_v, "K and V must have the same rows")
     dev = C.k.device
-    _on_device(f, dev, C.v, C.k_scale, C.v_scale, K, V, page_table, lens, off, ws)
-    seq = _sequences(f, K.shape[0], page_table, lens, off, max_new)
-    if K.shape[0] == 0:
+    _on_device(f, dev, K, V, page_table, lens, off, ws)
+    seq = _sequences(f, rows, page_table, lens, off, max_new)
+    if rows == 0:
         return
     handle, scope = _scope(dev, stream)
     with scope:
         if ws is None:
             ws = new_workspace(cache_append_workspace_bytes(), dev)
-        c = C.struct()
-        _check("hyb_cache_append", lib().hyb_cache_append(
-            ctypes.byref(c), ctypes.byref(seq), K.data_ptr(), ldk, hsk, V.data_ptr(), ldv, hsv,
-            ws.data_ptr(), ws.numel(), handle))
+        rc = lib().hyb_cache_append(ctypes.byref(c), ctypes.byref(seq), K.data_ptr(), ldk, hsk,
+                                    V.data_ptr(), ldv, hsv, ws.data_ptr(), ws.numel(), handle)
+    _check("hyb_cache_append", rc)
 
 
 def cache_attention_workspace_bytes(C: Cache, batch: int, heads: int, max_new: int,
@@ -960,29 +983,31 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     Returns O (bf16, as Q), with return_lse also the fp32 log-sum-exp
     [rows][heads]."""
     f = "cache_attention"
-    dim = C.k.shape[3]
-    ldq, hsq = _heads(f, Q, None, dim, "Q")
-    rows, heads = Q.shape[0], Q.shape[1]
+    c = C._struct
+    dim = c.head_dim
+    rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
     dev = C.k.device
-    _on_device(f, dev, C.v, C.k_scale, C.v_scale, Q, page_table, lens, off, out, ws)
+    _on_device(f, dev, Q, page_table, lens, off, out, ws)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
+    if out is not None:
+        out_rows, _, ldo, hso = _heads(f, out, heads, dim, "out")
+        _want(f, out_rows == rows, "out must have Q's shape")
+    else:
+        ldo, hso = heads * dim, dim
     handle, scope = _scope(dev, stream)
     with scope:
         if out is None:
-            out = torch.empty(rows, heads, dim, dtype=torch.bfloat16, device=dev)
-            ldo, hso = heads * dim, dim
-        else:
-            _want(f, out.shape == Q.shape, "out must have Q's shape")
-            ldo, hso = _heads(f, out, heads, dim, "out")
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev) if return_lse else None
+            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+        rc = HYB_OK
         if rows:
             if ws is None:
                 ws = new_workspace(cache_attention_workspace_bytes(
-                    C, seq.batch, heads, seq.max_new, seq.max_pages * C.page_size), dev)
-            c = C.struct()
-            _check("hyb_cache_attention", lib().hyb_cache_attention(
+                    C, seq.batch, heads, seq.max_new, seq.max_pages * c.page_size), dev)
+            rc = lib().hyb_cache_attention(
                 ctypes.byref(c), ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo,
                 hso, lse.data_ptr() if return_lse else None, heads, heads,
                 dim ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),
-                handle))
+                handle)
+    _check("hyb_cache_attention", rc)
     return (out, lse) if return_lse else out
