@@ -11,7 +11,7 @@
 //
 // every operation rounded to fp32 once, the last one to e4m3 (round to nearest
 // even, saturating at +-448; a NaN stays a NaN).
-#include "hyb_internal.cuh"
+#include "hyb_fp8.cuh"
 
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
@@ -21,7 +21,6 @@ namespace cg = cooperative_groups;
 namespace hyb {
 namespace {
 
-constexpr int kBlk = 128;               // columns per scale
 constexpr float kE4m3Max = 448.0f;
 // blocks whose largest value is smaller quantise as if it were this (an all-
 // zero block then needs no case of its own): 448 * 2^-64
@@ -98,6 +97,8 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(int64_t rows, int64
                                                              uint8_t *Q, int64_t ldq,
                                                              float *scale, int64_t lds,
                                                              int64_t cb, bool vec, uint32_t *status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 15;
   const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const unsigned half = 0xFFFFu << (threadIdx.x & 16);
@@ -168,53 +169,42 @@ __global__ void __launch_bounds__(256) fp8_quant_blocks_kernel(int64_t rows, int
   if (bad) atomicOr(status, kStatusNaN);
 }
 
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), dim3 grid, bool overlap, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
+}
+
 int quant_launch(int64_t rows, int64_t cols, const void *X, int64_t ldx, hyb_dtype xdt,
                  int block_rows, uint8_t *Q, int64_t ldq, float *scale, int64_t lds,
-                 uint32_t *status, cudaStream_t st) {
+                 uint32_t *status, bool overlap, cudaStream_t st) {
   const int64_t cb = (cols + kBlk - 1) / kBlk;
   const bool vec = (uintptr_t)X % 16 == 0 && ldx % (xdt == HYB_F32 ? 4 : 8) == 0;
   if (block_rows == 1) {
     const int64_t ctas = (rows * cb + 15) / 16;
     if (ctas > INT32_MAX) return HYB_ERR_UNSUPPORTED;
-    if (xdt == HYB_F32)
-      fp8_quant_rows_kernel<true><<<(unsigned)ctas, 256, 0, st>>>(rows, cols, X, ldx, Q, ldq,
-                                                                  scale, lds, cb, vec, status);
-    else
-      fp8_quant_rows_kernel<false><<<(unsigned)ctas, 256, 0, st>>>(rows, cols, X, ldx, Q, ldq,
-                                                                   scale, lds, cb, vec, status);
-  } else {
-    const int64_t rb = (rows + kBlk - 1) / kBlk;
-    if (rb > 65535 || cb > INT32_MAX) return HYB_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)cb, (unsigned)rb);
-    if (xdt == HYB_F32)
-      fp8_quant_blocks_kernel<true><<<grid, 256, 0, st>>>(rows, cols, X, ldx, Q, ldq, scale, lds,
-                                                          vec, status);
-    else
-      fp8_quant_blocks_kernel<false><<<grid, 256, 0, st>>>(rows, cols, X, ldx, Q, ldq, scale, lds,
-                                                           vec, status);
+    return launch(xdt == HYB_F32 ? fp8_quant_rows_kernel<true> : fp8_quant_rows_kernel<false>,
+                  dim3((unsigned)ctas), overlap, st, rows, cols, X, ldx, Q, ldq, scale, lds, cb,
+                  vec, status);
   }
-  return cudaGetLastError() == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
+  const int64_t rb = (rows + kBlk - 1) / kBlk;
+  if (rb > 65535 || cb > INT32_MAX) return HYB_ERR_UNSUPPORTED;
+  return launch(xdt == HYB_F32 ? fp8_quant_blocks_kernel<true> : fp8_quant_blocks_kernel<false>,
+                dim3((unsigned)cb, (unsigned)rb), overlap, st, rows, cols, X, ldx, Q, ldq, scale,
+                lds, vec, status);
 }
 
 // ---------------------------------------------------------------------------
 // skinny product
 // ---------------------------------------------------------------------------
-
-struct Fp8Params {
-  int64_t n, k, m;
-  const uint8_t *W;
-  int64_t ldw;
-  const float *sw;
-  int64_t ldsw;
-  const void *X;
-  int64_t ldx;
-  const float *sx;
-  int64_t ldsx;
-  void *Y;
-  int64_t ldy;
-  int bf16_out;
-  uint32_t *status;
-};
 
 // D += A B, one m16n8k32 e4m3 product with fp32 accumulation
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -452,6 +442,14 @@ int launch_skinny(const Fp8Params &p, int C, bool overlap, cudaStream_t st) {
              : HYB_ERR_CUDA;
 }
 
+// the most tokens that the skinny kernel takes
+constexpr int kSkinnyTokens = 16;
+
+// X's values in the workspace, behind its scales
+size_t fp8_x_offset(int64_t m, int64_t k) {
+  return align_up(kHeaderBytes + (size_t)m * (size_t)((k + kBlk - 1) / kBlk) * 4, 256);
+}
+
 int fp8_check(const hyb_fp8_matrix *A) {
   if (!A || !A->q || !A->scale) return HYB_ERR_INVALID_ARG;
   if (A->n < 1 || A->k < 1 || A->ldq < A->k || A->lds < (A->k + kBlk - 1) / kBlk)
@@ -483,12 +481,14 @@ int hyb_fp8_quant(int64_t rows, int64_t cols, const void *X, int64_t ldx, hyb_dt
   if (!ws || ws_bytes < kHeaderBytes) return HYB_ERR_WORKSPACE;
   if ((uintptr_t)ws % 256 != 0) return HYB_ERR_ALIGNMENT;
   return quant_launch(rows, cols, X, ldx, xdt, block_rows, Q, ldq, scale, lds,
-                      static_cast<uint32_t *>(ws), (cudaStream_t)stream);
+                      static_cast<uint32_t *>(ws), false, (cudaStream_t)stream);
 }
 
+// workspace: header; for the tensor-core product also X's scales and values
 size_t hyb_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m < 1 || n < 1 || k < 1 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX - kBlk) return 0;
-  return kHeaderBytes;
+  if (m <= kSkinnyTokens) return kHeaderBytes;
+  return fp8_x_offset(m, k) + (size_t)m * align_up((size_t)k, 16);
 }
 
 int hyb_fp8_matmul(const hyb_fp8_matrix *A, int64_t m, const void *X, int64_t ldx, hyb_dtype xdt,
@@ -528,6 +528,21 @@ int hyb_fp8_matmul(const hyb_fp8_matrix *A, int64_t m, const void *X, int64_t ld
   const bool overlap = (flags & HYB_LAUNCH_OVERLAP_PREV) != 0;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf = xdt == HYB_BF16;
+  if (m > kSkinnyTokens) {
+    if (bf) {
+      uint8_t *base = static_cast<uint8_t *>(ws);
+      float *sx = reinterpret_cast<float *>(base + kHeaderBytes);
+      uint8_t *xq = base + fp8_x_offset(m, A->k);
+      const int64_t ld = (int64_t)align_up((size_t)A->k, 16);
+      rc = quant_launch(m, A->k, X, ldx, HYB_BF16, 1, xq, ld, sx, kb, p.status, overlap, st);
+      if (rc != HYB_OK) return rc;
+      p.X = xq;
+      p.ldx = ld;
+      p.sx = sx;
+      p.ldsx = kb;
+    }
+    return fp8_gemm(p, bf || overlap, st);
+  }
   if (m <= 8)
     return bf ? launch_skinny<1, 2, 1, true>(p, 4, overlap, st)
               : launch_skinny<1, 2, 1, false>(p, 4, overlap, st);

@@ -1,0 +1,326 @@
+// The 8-bit floating-point product for more than a few tokens, on the 5th-
+// generation tensor cores:
+//
+//   Y[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in block b} xq[m][k] wq[n][k]
+//
+// tcgen05.mma multiplies a block of 128 columns exactly as the sum over k asks
+// (e4m3 x e4m3 products are exact, accumulation in fp32), but the scales change
+// from block to block, so a block's products go to a tensor-memory buffer of
+// their own and the epilogue warps add them, scaled, to fp32 sums in registers
+// while the tensor cores fill the other buffer.
+//
+//   * A CTA owns 128 tokens (the MMA's M, one tensor-memory lane each) and BN
+//     rows of W (its N).  With the tokens in the lanes a thread's token scale is
+//     one register and W's scale one per 128 columns: a block costs one FMA per
+//     value and no other scale traffic.
+//   * warp 0 moves operand blocks with TMA (128-byte rows in the 128-byte
+//     swizzle: one block of k is one swizzle row), warp 1 issues the MMAs, warps
+//     2-9 (two per lane quarter, half of the columns each) scale and add.
+//   * Where the tiles alone do not fill the GPU, a cluster of CTAs splits k; its
+//     partial sums meet in distributed shared memory in a fixed order.
+#include "hyb_fp8.cuh"
+#include "hyb_tcgen05.cuh"
+
+#include <cooperative_groups.h>
+
+namespace cg = cooperative_groups;
+
+namespace hyb {
+namespace {
+
+constexpr int kTok = 128;       // tokens per CTA
+constexpr int kThreads = 320;   // producer, MMA, 8 epilogue warps
+
+template <int BN>
+struct Shape {
+  static constexpr int kStage = (kTok + BN) * kBlk;  // bytes of one block's operands
+  static constexpr int kStages = BN == 256 ? 4 : 3;
+  static constexpr int kRing = kStage * kStages;
+  static constexpr int kCols = BN / 2;               // columns per epilogue thread
+  static constexpr int kPitch = BN + 4;              // floats per row of the result in shared memory
+  static constexpr int kTmem = 2 * BN;
+  static_assert(kTok * kPitch * 4 <= kRing, "the result reuses the ring");
+  static_assert(kStage % 1024 == 0, "swizzle alignment");
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t accumulate, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %4, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(accumulate), "r"(idesc)
+      : "memory");
+}
+
+// 16 columns of this thread's lane; the values are there after tmem_wait16
+__device__ __forceinline__ void tmem_issue16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads)
+    fp8_gemm_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap xmap,
+                    const __grid_constant__ CUtensorMap wmap) {
+  using Sh = Shape<BN>;
+  constexpr int NS = Sh::kStages;
+  // D fp32, A and B e4m3 (format 0), K-major, N = BN, M = 128
+  constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kTok >> 4) << 24);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], tfull[2], tempty[2];
+  __shared__ uint32_t s_tmem;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t n0 = (int64_t)(blockIdx.x / C) * BN, m0 = (int64_t)blockIdx.y * kTok;
+  const int kb = (int)((p.k + kBlk - 1) / kBlk);
+  const int b0 = (int)((int64_t)kb * rank / C), nb = (int)((int64_t)kb * (rank + 1) / C) - b0;
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 256);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(Sh::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      bool waited = false;
+      for (int j = 0; j < nb && ok; ++j) {
+        const int s = j % NS;
+        ok = ring_wait(&empty[s], ((uint32_t)(j / NS) & 1u) ^ 1u);
+        if (!ok) break;
+        uint8_t *st = smem + (size_t)s * Sh::kStage;
+        mbar_arrive_expect_tx(&full[s], Sh::kStage);
+        // W is no output of the preceding kernel; X (or its scales) may be
+        tma_load_2d(st + kTok * kBlk, &wmap, (b0 + j) * kBlk, (int)n0, &full[s]);
+        if (!waited) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");
+          waited = true;
+        }
+        tma_load_2d(st, &xmap, (b0 + j) * kBlk, (int)m0, &full[s]);
+      }
+      if (!ok) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int j = 0; j < nb && ok; ++j) {
+        const int s = j % NS, buf = j & 1;
+        ok = ring_wait(&full[s], (uint32_t)(j / NS) & 1u) &&
+             ring_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + (size_t)s * Sh::kStage), b = a + kTok * kBlk;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 columns (32 bytes of the swizzle row) at a time
+          umma_f8(tmem + buf * BN, sw128_desc(a + kk * 32), sw128_desc(b + kk * 32), kk != 0,
+                  kIdesc);
+        umma_commit(&empty[s]);
+        umma_commit(&tfull[buf]);
+      }
+      if (!ok) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else {
+    const int half = (warp - 2) >> 2;
+    const int row = 32 * (warp & 3) + lane;  // this thread's token, its tensor-memory lane
+    const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(half * Sh::kCols);
+    float acc[Sh::kCols];
+#pragma unroll
+    for (int c = 0; c < Sh::kCols; ++c) acc[c] = 0.0f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *sxp = p.sx + min(m0 + row, p.m - 1) * p.ldsx + b0;
+    // the scale of this thread's columns (they lie in one block of 128 rows of W)
+    const float *swp = p.sw + min(n0 + half * Sh::kCols, p.n - 1) / kBlk * p.ldsw + b0;
+    float sx = 0.0f, sw = 0.0f;
+    if (nb > 0) {
+      sx = __ldg(sxp);
+      sw = __ldg(swp);
+    }
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      const int buf = j & 1;
+      const float s = sx * sw;
+      if (j + 1 < nb) {
+        sx = __ldg(sxp + j + 1);
+        sw = __ldg(swp + j + 1);
+      }
+      ok = ring_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t d[2][16];
+      tmem_issue16(tbase + buf * BN, d[0]);
+#pragma unroll
+      for (int c = 0; c < Sh::kCols / 16; ++c) {
+        tmem_wait16(d[c & 1]);
+        if (c + 1 < Sh::kCols / 16) {
+          tmem_issue16(tbase + buf * BN + 16 * (c + 1), d[(c + 1) & 1]);
+        } else {
+          tc_fence_before();
+          mbar_arrive(&tempty[buf]);
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          acc[16 * c + q] = fmaf(__uint_as_float(d[c & 1][q]), s, acc[16 * c + q]);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+    // every epilogue thread is past its last block: the MMAs have read the ring
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    float *out = reinterpret_cast<float *>(smem) + row * Sh::kPitch + half * Sh::kCols;
+#pragma unroll
+    for (int c = 0; c < Sh::kCols; c += 4)
+      *reinterpret_cast<float4 *>(out + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+  }
+  tc_fence_before();
+  cluster.sync();  // also the CTA's own barrier
+
+  // the cluster's CTAs share the rows: a warp takes a row of BN sums at a time
+  {
+    const int rows = (int)min((int64_t)kTok, p.m - m0);
+    const float *mine = reinterpret_cast<const float *>(smem);
+    const int es = p.bf16_out ? 2 : 4;
+    const bool vec = ((uintptr_t)p.Y % 16 == 0) && (p.ldy * es % 16 == 0);
+    for (int r = rank + C * warp; r < rows; r += C * (kThreads / 32)) {
+      for (int c = lane * 8; c < BN; c += 256) {
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int q = 0; q < C; ++q) {
+          const float *src = C == 1 ? mine : cluster.map_shared_rank(mine, q);
+          const float4 a = *reinterpret_cast<const float4 *>(src + r * Sh::kPitch + c);
+          const float4 b = *reinterpret_cast<const float4 *>(src + r * Sh::kPitch + c + 4);
+          v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+          v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+        }
+        const int64_t n = n0 + c, at = (m0 + r) * p.ldy + n;
+        if (p.bf16_out) {
+          uint16_t *y = static_cast<uint16_t *>(p.Y) + at;
+          if (vec && n + 8 <= p.n) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              w[q] = f32_to_bf16_rne(v[2 * q]) | ((uint32_t)f32_to_bf16_rne(v[2 * q + 1]) << 16);
+            *reinterpret_cast<uint4 *>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (n + q < p.n) y[q] = f32_to_bf16_rne(v[q]);
+          }
+        } else {
+          float *y = static_cast<float *>(p.Y) + at;
+          if (vec && n + 8 <= p.n) {
+            reinterpret_cast<float4 *>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (n + q < p.n) y[q] = v[q];
+          }
+        }
+      }
+    }
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(Sh::kTmem)
+                 : "memory");
+  }
+}
+
+// [rows][k] bytes, boxes of 128 columns x box_rows rows in the 128-byte swizzle
+int encode_bytes(const void *base, int64_t k, int64_t rows, int64_t ld, int box_rows,
+                 CUtensorMap *map) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return HYB_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlk, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult res = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS ? HYB_OK : HYB_ERR_CUDA;
+}
+
+template <int BN>
+int launch_gemm(const Fp8Params &p, int C, bool after_quant, cudaStream_t st) {
+  using Sh = Shape<BN>;
+  const int64_t tiles = (p.n + BN - 1) / BN, toks = (p.m + kTok - 1) / kTok;
+  if (tiles * C > INT32_MAX || toks > 65535) return HYB_ERR_UNSUPPORTED;
+  alignas(64) CUtensorMap xmap{}, wmap{};
+  int rc = encode_bytes(p.X, p.k, p.m, p.ldx, kTok, &xmap);
+  if (rc == HYB_OK) rc = encode_bytes(p.W, p.k, p.n, p.ldw, BN, &wmap);
+  if (rc != HYB_OK) return rc;
+  const int dyn = Sh::kRing + 1024;
+  if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           dyn) != cudaSuccess)
+    return HYB_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * C), (unsigned)toks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after_quant ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN>, p, xmap, wmap) == cudaSuccess
+             ? HYB_OK
+             : HYB_ERR_CUDA;
+}
+
+}  // namespace
+
+int fp8_gemm(const Fp8Params &p, bool after_quant, cudaStream_t st) {
+  int sms;
+  const int rc = device_sm_count(&sms);
+  if (rc != HYB_OK) return rc;
+  const int64_t toks = (p.m + kTok - 1) / kTok;
+  const int64_t kb = (p.k + kBlk - 1) / kBlk;
+  const int64_t wide = (p.n + 255) / 256 * toks;
+  if (wide >= sms) return launch_gemm<256>(p, 1, after_quant, st);
+  const int64_t tiles = (p.n + 127) / 128 * toks;
+  int C = 1;
+  while (C < 8 && tiles * C * 2 <= 2 * sms && kb >= 4 * C) C *= 2;
+  return launch_gemm<128>(p, C, after_quant, st);
+}
+
+}  // namespace hyb

@@ -45,6 +45,7 @@
 // work.  Every wait is bounded; one that runs out sets kStatusTimeout in the
 // status word and the CTA leaves its pipeline.
 #include "hyb_internal.cuh"
+#include "hyb_tcgen05.cuh"
 
 namespace hyb {
 namespace {
@@ -113,19 +114,7 @@ __device__ __forceinline__ uint64_t e_desc(uint32_t saddr) {
   return d;
 }
 
-// Shared-memory matrix descriptor of a K-major operand in the 128-byte
-// swizzle layout: rows 128 bytes apart, 8-row groups 1024 bytes apart
-// (stride byte offset), descriptor version 1, layout type 2 (128B swizzle).
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;             // leading byte offset (unused by swizzled K-major)
-  d |= (uint64_t)(1024 >> 4) << 32;   // stride byte offset
-  d |= (uint64_t)1 << 46;             // version
-  d |= (uint64_t)2 << 61;             // 128-byte swizzle
-  return d;
-}
-
-// The same for the 64-byte swizzle layout: rows 64 bytes apart, 8-row groups
+// As sw128_desc for the 64-byte swizzle layout: rows 64 bytes apart, 8-row groups
 // 512 bytes apart, layout type 4 (a 2:4 tile's half: 32 kept values per row).
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
   uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
@@ -161,55 +150,6 @@ __device__ __forceinline__ void umma_sp_bf16(uint32_t tmem_d, uint64_t adesc, ui
 __device__ __forceinline__ void tmem_cp_128x128b(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.128x128b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-// arrives on the mbarrier once every tcgen05.mma this thread issued before
-// has completed
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::
-                   "r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-// 16 consecutive fp32 columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
-}
-
-// Waits for the mbarrier phase of the given parity.  The thread sleeps in
-// mbarrier.try_wait with an explicit suspend-time hint: in this pipeline a
-// blocked try_wait without one woke up late enough to cost most of a
-// microsecond per ring slot.  Gives up (returns false) after about 2^31 SM
-// clocks, so a phase that never completes ends the CTA's pipeline.
-__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
-  const long long t0 = clock64();
-  do {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(200000u)  // hint: 200 us
-        : "memory");
-    if (ok) return true;
-  } while (clock64() - t0 < (1ll << 31));
-  return false;
-}
-
 struct PrefillParams {
   const uint8_t *map;
   const uint16_t *vals;
