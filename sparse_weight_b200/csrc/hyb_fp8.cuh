@@ -6,8 +6,69 @@
 namespace hyb {
 
 constexpr int kBlk = 128;  // columns (and rows of W) per scale
+// The most tokens of the decode kernel: its rows are one warp's lanes.
+constexpr int kDecodeTokens = 32;
+// The largest weight of the small kernel.
+constexpr int64_t kSmallBytes = 8 << 20;
+constexpr float kE4m3Max = 448.0f;
+// blocks whose largest value is smaller quantise as if it were this (an all-
+// zero block then needs no case of its own): 448 * 2^-64
+constexpr float kMinAmax = 448.0f / 18446744073709551616.0f;
 
-// One product: W [n][k] and X [m][k] e4m3 (X bf16 where the skinny kernel
+// largest finite |x| so far; flags a NaN or an infinity
+__device__ __forceinline__ void amax_finite(float x, float &a, bool &bad) {
+  const float v = fabsf(x);
+  const bool fin = v <= 3.402823466e38f;  // false for NaN and infinity
+  bad |= !fin;
+  a = fmaxf(a, fin ? v : 0.0f);
+}
+
+// two fp32 -> two e4m3 bytes (lo in the low byte), round to nearest even,
+// saturating; NaN -> 0x7F
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+
+// 8 consecutive values of a row as fp32; those at or past `left` read as zero.
+// `vec`: the rows start on 16 bytes (else they are read value by value).
+template <bool F32>
+__device__ __forceinline__ void load8(const void *X, int64_t off, int left, bool vec,
+                                      float (&v)[8]) {
+  if (left >= 8 && vec) {
+    if constexpr (F32) {
+      const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(X) + off);
+      const float4 a = __ldg(p), b = __ldg(p + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 r = ld_keep16(static_cast<const uint16_t *>(X) + off);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.0f;
+      if (i < left) {
+        if constexpr (F32)
+          v[i] = static_cast<const float *>(X)[off + i];
+        else
+          v[i] = __uint_as_float((uint32_t) static_cast<const uint16_t *>(X)[off + i] << 16);
+      }
+    }
+  }
+}
+
+// One product: W [n][k] and X [m][k] e4m3 (X bf16 where the small kernel
 // quantises it itself), their scales, and Y.
 struct Fp8Params {
   int64_t n, k, m;
@@ -21,13 +82,44 @@ struct Fp8Params {
   int64_t ldsx;
   void *Y;
   int64_t ldy;
-  int bf16_out;
+  int bf16_out, x_bf16;
+  int early_w;  // W may be read before the preceding kernel has ended
   uint32_t *status;
 };
 
-// The tensor-core product (hyb_fp8_gemm.cu) of e4m3 operands.  `after_quant`:
-// X and its scales come from the kernel queued just before (programmatic
-// dependent launch).
-int fp8_gemm(const Fp8Params &p, bool after_quant, cudaStream_t st);
+// All of these kernels are programmatic dependents of whatever precedes them on
+// the stream: their CTAs start while it ends, and each waits
+// (griddepcontrol.wait) for its completion before it touches memory, but for
+// reads of W where early_w allows them.  Every CTA waits, so that a kernel's end
+// also means the end of all before it.
+
+// The tensor-core product (hyb_fp8_gemm.cu) of e4m3 operands.
+int fp8_gemm(const Fp8Params &p, cudaStream_t st);
+// The same for m <= kDecodeTokens.
+int fp8_decode(const Fp8Params &p, cudaStream_t st);
+// The same for few tokens and a small weight (hyb_fp8_small.cu), of X in bf16
+// or e4m3.
+bool fp8_is_small(int64_t m, int64_t n, int64_t k);
+int fp8_small(const Fp8Params &p, cudaStream_t st);
+
+// A launch as a programmatic dependent, in clusters of C CTAs along x.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, int C,
+                     cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
+}
 
 }  // namespace hyb

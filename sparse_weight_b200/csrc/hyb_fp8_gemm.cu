@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads)
   const int kb = (int)((p.k + kBlk - 1) / kBlk);
   const int b0 = (int)((int64_t)kb * rank / C), nb = (int)((int64_t)kb * (rank + 1) / C) - b0;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(kThreads)
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      bool waited = false;
+      bool waited = !p.early_w;
+      if (waited) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int j = 0; j < nb && ok; ++j) {
         const int s = j % NS;
         ok = ring_wait(&empty[s], ((uint32_t)(j / NS) & 1u) ^ 1u);
@@ -205,7 +207,8 @@ __global__ void __launch_bounds__(kThreads)
       *reinterpret_cast<float4 *>(out + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
   }
   tc_fence_before();
-  cluster.sync();  // also the CTA's own barrier
+  __syncthreads();  // warps that wait here do not poll, as they would in the cluster's barrier
+  if (C > 1) cluster.sync();
 
   // the cluster's CTAs share the rows: a warp takes a row of BN sums at a time
   {
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
   }
-  cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -277,7 +280,7 @@ int encode_bytes(const void *base, int64_t k, int64_t rows, int64_t ld, int box_
 }
 
 template <int BN>
-int launch_gemm(const Fp8Params &p, int C, bool after_quant, cudaStream_t st) {
+int launch_gemm(const Fp8Params &p, int C, cudaStream_t st) {
   using Sh = Shape<BN>;
   const int64_t tiles = (p.n + BN - 1) / BN, toks = (p.m + kTok - 1) / kTok;
   if (tiles * C > INT32_MAX || toks > 65535) return HYB_ERR_UNSUPPORTED;
@@ -289,38 +292,280 @@ int launch_gemm(const Fp8Params &p, int C, bool after_quant, cudaStream_t st) {
   if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            dyn) != cudaSuccess)
     return HYB_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * C), (unsigned)toks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = dyn;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after_quant ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<BN>, p, xmap, wmap) == cudaSuccess
-             ? HYB_OK
-             : HYB_ERR_CUDA;
+  return launch_dependent(fp8_gemm_kernel<BN>, dim3((unsigned)(tiles * C), (unsigned)toks), kThreads, dyn, C, st, p,
+                          xmap, wmap);
+}
+
+// ---------------------------------------------------------------------------
+// decode
+// ---------------------------------------------------------------------------
+//
+// The same product for m <= 32 tokens, which is bound by W's bytes: the tokens
+// fill one warp's lanes of the MMA's 128 rows and the other lanes' products are
+// not looked at (the MMA unit has the time, and its operand rows 32 .. 127 are
+// whatever lies behind X's 4 KB: W's tile, and behind a narrow one the next
+// stage's).  Two warps, half of the columns each, scale and add.  Quantising a
+// bf16 X in this kernel, by the warps that are idle, was slower than a kernel
+// before it that this one overlaps (16 x 4096 x 14336: 27 us and 18 us): every
+// row tile does that work again.
+
+// warps 0 and 4 (whose tensor-memory lanes hold the tokens): epilogue; 1: MMA;
+// 2: TMA
+constexpr int kDecodeThreads = 160;
+
+template <int BN>
+struct DecodeShape {
+  static constexpr int kStage = (kDecodeTokens + BN) * kBlk;
+  static constexpr int kStages = BN == 128 ? 5 : 8;
+  static constexpr int kTail = kTok * kBlk > kStage ? kTok * kBlk - kStage : 0;
+  static constexpr int kBytes = kStage * kStages + kTail;
+  static constexpr int kCols = BN / 2;
+  static constexpr int kPitch = BN + 4;
+  static constexpr int kTmem = 2 * BN;
+  static_assert(kDecodeTokens * kPitch * 4 <= kStage * kStages, "the result reuses the ring");
+  static_assert(kStage % 1024 == 0, "swizzle alignment");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kDecodeThreads, 2)
+    fp8_decode_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap xmap,
+                      const __grid_constant__ CUtensorMap wmap) {
+  using Sh = DecodeShape<BN>;
+  constexpr int NS = Sh::kStages;
+  constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kTok >> 4) << 24);
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], tfull[2], tempty[2];
+  __shared__ uint32_t s_tmem;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t n0 = (int64_t)(blockIdx.x / C) * BN;
+  const int kb = (int)((p.k + kBlk - 1) / kBlk);
+  const int b0 = (int)((int64_t)kb * rank / C), nb = (int)((int64_t)kb * (rank + 1) / C) - b0;
+  const int m = (int)p.m;
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  auto load_w = [&](int j) {
+    const int s = j % NS;
+    mbar_arrive_expect_tx(&full[s], Sh::kStage);
+    tma_load_2d(smem + (size_t)s * Sh::kStage + kDecodeTokens * kBlk, &wmap, (b0 + j) * kBlk,
+                (int)n0, &full[s]);
+  };
+  if (tid == 64) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], 64);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // W's first blocks set out before anything else is ready
+    if (!p.early_w) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int j = 0; j < min(nb, NS); ++j) load_w(j);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(Sh::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp == 2) {
+    if (lane == 0) {
+      bool ok = true;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int j = 0; j < nb && ok; ++j) {
+        const int s = j % NS;
+        if (j >= NS) {
+          ok = ring_wait(&empty[s], ((uint32_t)(j / NS) & 1u) ^ 1u);
+          if (!ok) break;
+          load_w(j);
+        }
+        tma_load_2d(smem + (size_t)s * Sh::kStage, &xmap, (b0 + j) * kBlk, 0, &full[s]);
+      }
+      if (!ok) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int j = 0; j < nb && ok; ++j) {
+        const int s = j % NS, buf = j & 1;
+        ok = ring_wait(&full[s], (uint32_t)(j / NS) & 1u) &&
+             ring_wait(&tempty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + (size_t)s * Sh::kStage), b = a + kDecodeTokens * kBlk;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f8(tmem + buf * BN, sw128_desc(a + kk * 32), sw128_desc(b + kk * 32), kk != 0,
+                  kIdesc);
+        umma_commit(&empty[s]);
+        umma_commit(&tfull[buf]);
+      }
+      if (!ok) atomicOr(p.status, kStatusTimeout);
+    }
+    __syncwarp();
+  } else if (warp != 3) {
+    // scale and add: lane = token (lanes 0 .. 31 of tensor memory), half of the columns
+    const int half = warp >> 2;
+    const uint32_t tbase = tmem + (uint32_t)(half * Sh::kCols);
+    float acc[Sh::kCols];
+#pragma unroll
+    for (int c = 0; c < Sh::kCols; ++c) acc[c] = 0.0f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float *sxp = p.sx + min(lane, m - 1) * p.ldsx + b0;
+    const float *swp = p.sw + min(n0 + half * Sh::kCols, p.n - 1) / kBlk * p.ldsw + b0;
+    float sx = 0.0f, sw = 0.0f;
+    if (nb > 0) {
+      sx = __ldg(sxp);
+      sw = __ldg(swp);
+    }
+    bool ok = true;
+    for (int j = 0; j < nb; ++j) {
+      const int buf = j & 1;
+      const float s = sx * sw;
+      if (j + 1 < nb) {
+        sx = __ldg(sxp + j + 1);
+        sw = __ldg(swp + j + 1);
+      }
+      ok = ring_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t d[2][16];
+      tmem_issue16(tbase + buf * BN, d[0]);
+#pragma unroll
+      for (int c = 0; c < Sh::kCols / 16; ++c) {
+        tmem_wait16(d[c & 1]);
+        if (c + 1 < Sh::kCols / 16) {
+          tmem_issue16(tbase + buf * BN + 16 * (c + 1), d[(c + 1) & 1]);
+        } else {
+          tc_fence_before();
+          mbar_arrive(&tempty[buf]);
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          acc[16 * c + q] = fmaf(__uint_as_float(d[c & 1][q]), s, acc[16 * c + q]);
+      }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+    if (lane < m) {  // past the last block: the MMAs have read the ring
+      float *out = reinterpret_cast<float *>(smem) + lane * Sh::kPitch + half * Sh::kCols;
+#pragma unroll
+      for (int c = 0; c < Sh::kCols; c += 4)
+        *reinterpret_cast<float4 *>(out + c) =
+            make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();  // warps that wait here do not poll, as they would in the cluster's barrier
+  if (C > 1) cluster.sync();
+
+  // the cluster's CTAs share the sums, four columns of a token at a time
+  {
+    const float *mine = reinterpret_cast<const float *>(smem);
+    const int es = p.bf16_out ? 2 : 4;
+    const bool vec = ((uintptr_t)p.Y % (4 * es) == 0) && (p.ldy % 4 == 0);
+    for (int e = rank + C * tid; e < m * (BN / 4); e += C * kDecodeThreads) {
+      const int r = e / (BN / 4), c = e % (BN / 4) * 4;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int q = 0; q < C; ++q) {
+        const float *src = C == 1 ? mine : cluster.map_shared_rank(mine, q);
+        const float4 a = *reinterpret_cast<const float4 *>(src + r * Sh::kPitch + c);
+        v.x += a.x;
+        v.y += a.y;
+        v.z += a.z;
+        v.w += a.w;
+      }
+      const int64_t n = n0 + c, at = r * p.ldy + n;
+      const float o[4] = {v.x, v.y, v.z, v.w};
+      if (p.bf16_out) {
+        uint16_t *y = static_cast<uint16_t *>(p.Y) + at;
+        if (vec && n + 4 <= p.n) {
+          *reinterpret_cast<uint2 *>(y) =
+              make_uint2(f32_to_bf16_rne(o[0]) | ((uint32_t)f32_to_bf16_rne(o[1]) << 16),
+                         f32_to_bf16_rne(o[2]) | ((uint32_t)f32_to_bf16_rne(o[3]) << 16));
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < p.n) y[q] = f32_to_bf16_rne(o[q]);
+        }
+      } else {
+        float *y = static_cast<float *>(p.Y) + at;
+        if (vec && n + 4 <= p.n) {
+          *reinterpret_cast<float4 *>(y) = v;
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < p.n) y[q] = o[q];
+        }
+      }
+    }
+  }
+  if (C > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(Sh::kTmem)
+                 : "memory");
+  }
+}
+
+template <int BN>
+int launch_decode(const Fp8Params &p, int C, cudaStream_t st) {
+  using Sh = DecodeShape<BN>;
+  const int64_t tiles = (p.n + BN - 1) / BN;
+  if (tiles * C > INT32_MAX) return HYB_ERR_UNSUPPORTED;
+  alignas(64) CUtensorMap xmap{}, wmap{};
+  int rc = encode_bytes(p.W, p.k, p.n, p.ldw, BN, &wmap);
+  if (rc == HYB_OK) rc = encode_bytes(p.X, p.k, p.m, p.ldx, kDecodeTokens, &xmap);
+  if (rc != HYB_OK) return rc;
+  const int dyn = Sh::kBytes + 1024;
+  if (cudaFuncSetAttribute(fp8_decode_kernel<BN>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+    return HYB_ERR_CUDA;
+  return launch_dependent(fp8_decode_kernel<BN>, dim3((unsigned)(tiles * C)), kDecodeThreads, dyn, C, st, p,
+                          xmap, wmap);
 }
 
 }  // namespace
 
-int fp8_gemm(const Fp8Params &p, bool after_quant, cudaStream_t st) {
+int fp8_decode(const Fp8Params &p, cudaStream_t st) {
+  int sms;
+  const int rc = device_sm_count(&sms);
+  if (rc != HYB_OK) return rc;
+  const int64_t kb = (p.k + kBlk - 1) / kBlk;
+  // two CTAs fit an SM; a cluster has at most 8 and each CTA at least 2 blocks
+  const bool narrow = (p.n + 127) / 128 * 8 < sms;
+  const int64_t tiles = narrow ? (p.n + 63) / 64 : (p.n + 127) / 128;
+  int64_t C = 2 * sms / tiles;
+  if (C > kb / 2) C = kb / 2;
+  C = C < 1 ? 1 : (C > 8 ? 8 : C);
+  return narrow ? launch_decode<64>(p, (int)C, st)
+                : launch_decode<128>(p, (int)C, st);
+}
+
+int fp8_gemm(const Fp8Params &p, cudaStream_t st) {
   int sms;
   const int rc = device_sm_count(&sms);
   if (rc != HYB_OK) return rc;
   const int64_t toks = (p.m + kTok - 1) / kTok;
   const int64_t kb = (p.k + kBlk - 1) / kBlk;
   const int64_t wide = (p.n + 255) / 256 * toks;
-  if (wide >= sms) return launch_gemm<256>(p, 1, after_quant, st);
+  if (wide >= sms) return launch_gemm<256>(p, 1, st);
   const int64_t tiles = (p.n + 127) / 128 * toks;
   int C = 1;
   while (C < 8 && tiles * C * 2 <= 2 * sms && kb >= 4 * C) C *= 2;
-  return launch_gemm<128>(p, C, after_quant, st);
+  return launch_gemm<128>(p, C, st);
 }
 
 }  // namespace hyb
