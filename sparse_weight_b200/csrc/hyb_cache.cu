@@ -29,10 +29,10 @@ struct SeqParams {
 // where the caller's arrays contradict one another.
 __device__ __forceinline__ bool sequence(const SeqParams &s, int b, uint32_t *status,
                                          int64_t &row0, int &fresh, int &len) {
-  len = __ldg(s.lens + b);
+  len = ld_dep(s.lens + b);
   bool ok = len >= 0 && (int64_t)len <= ((int64_t)s.max_pages << s.page_shift);
   if (s.off) {
-    const int64_t o0 = __ldg(s.off + b), o1 = __ldg(s.off + b + 1);
+    const int64_t o0 = ld_dep(s.off + b), o1 = ld_dep(s.off + b + 1);
     ok &= o0 >= 0 && o0 <= o1 && o1 <= s.rows && o1 - o0 <= s.max_new;
     row0 = o0;
     fresh = (int)(o1 - o0);
@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
   constexpr int TPP = 128 / LANES;     // tokens per pass
   constexpr int PASSES = 64 / TPP;     // for the largest page
   __shared__ float s_a[4];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = blockIdx.z, h = blockIdx.y;
   const int which = blockIdx.x & 1, nth = blockIdx.x >> 1;
   int64_t row0;
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
   const int P = 1 << p.s.page_shift;
   const int slot = (start >> p.s.page_shift) + nth;
   if (((int64_t)slot << p.s.page_shift) >= len) return;
-  const int page = __ldg(p.s.table + b * p.s.table_stride + slot);
+  const int page = ld_dep(p.s.table + b * p.s.table_stride + slot);
   if (page < 0 || page >= p.num_pages) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeq);
     return;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
   const int lo = max(start - t0, 0), hi = min(len - t0, P);  // its new tokens
   const int c = threadIdx.x % LANES, tok0 = threadIdx.x / LANES;
   float *sc = p.scale[which] + (int64_t)page * p.kv_heads + h;
-  const float had = lo > 0 ? *sc : 0.0f;
+  const float had = lo > 0 ? ld_dep(sc) : 0.0f;
   uint8_t *q = p.q[which] + page * p.sp + h * p.sh + c * 8;
   const uint16_t *x = p.x[which] + h * p.hsx[which] + c * 8;
 
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
     const int tok = j * TPP + tok0;
     raw[j] = make_uint4(0, 0, 0, 0);
     if (tok >= lo && tok < hi)
-      raw[j] = ld_keep16(x + (row0 + (t0 + tok - start)) * p.ldx[which]);
+      raw[j] = ld_dep16(x + (row0 + (t0 + tok - start)) * p.ldx[which]);
   }
 #pragma unroll
   for (int j = 0; j < PASSES; ++j) {
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
     const float ratio = __fdiv_rn(had, scale);
     for (int tok = tok0; tok < lo; tok += TPP) {
       uint2 *at = reinterpret_cast<uint2 *>(q + tok * p.st);
-      const uint2 o = *at;
+      const uint2 o = __ldcg(at);
       uint32_t w[2] = {o.x, o.y};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -190,10 +192,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
 // attention
 // ---------------------------------------------------------------------------
 
-constexpr int kStep = 32;   // tokens per step of a warp
-constexpr int kRows = 16;   // query rows (new token x head of the group) per unit
-constexpr int kWarps = 4;   // warps of a CTA, each with its own steps
-constexpr int kStages = 3;  // steps in flight per warp
+constexpr int kStep = 32;   // tokens per step
+constexpr int kWarps = 4;   // warps that compute
 // probabilities are held times 2^15 (exp2 of t - max + 15): fp16's 11 bits then
 // reach down to 2^-29 of the largest one and its steps to 2^-39
 constexpr float kLift = 15.0f;
@@ -279,31 +279,64 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// A unit is 16 query rows (new token x head of the group) of one sequence and
-// one key / value head; its visible tokens are cut into steps of 32, the steps
-// into `splits` CTAs and there over 4 warps.  Each warp runs its own ring of
-// TMA boxes and its own running maximum and sum; the CTA's warps, then the
-// unit's CTAs, are merged in a fixed order.
+// transpose of an 8 x 8 matrix of fp16 held by the warp
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// What a CTA's shape is: NR tiles of 8 query rows (new token x head of the
+// group) per warp.  Split tokens (SHARE false): the 4 warps take the unit's
+// steps of 32 tokens in turn, each through a ring of its own, and are merged.
+// Split rows (SHARE true): the warps have their own rows and share one ring,
+// which a fifth warp fills.
+template <int D, int NR, bool SHARE>
+struct AttnShape {
+  static constexpr int kRows = 8 * NR * (SHARE ? kWarps : 1);  // of a unit
+  static constexpr int kBox = kStep * D;                       // a step's keys (or values), bytes
+  static constexpr int kStages = SHARE ? 4 : 2;                // per ring
+  static constexpr int kRing = kStages * 2 * kBox;
+  static constexpr int kRings = SHARE ? 1 : kWarps;
+  static constexpr int kThreads = 32 * (kWarps + (SHARE ? 1 : 0));
+  static constexpr int kPitch = D + 4;                         // floats per row of a warp's result
+  static constexpr int kOut = 8 * NR * kPitch * 4;             // bytes of it
+  static constexpr int kWarpOut = SHARE ? kOut : kRing;        // from one warp's to the next's
+  static constexpr int kBytes = kRing * kRings > kWarps * kWarpOut ? kRing * kRings : kWarps * kWarpOut;
+  static constexpr int kPart = kRows * D + 2 * kRows;          // floats of a CTA's partial result
+  static_assert(SHARE || kOut <= kRing, "a warp's result fits its ring");
+};
+
+// A unit is kRows query rows of one sequence and one key / value head; its
+// visible tokens are cut into steps of 32 and the steps into `splits` CTAs,
+// which are merged in a fixed order.
 //
 // Both products run as m16n8k16 on fp16 fragments built from the 8-bit bytes
-// in registers.  A product's sum over k does not care which column sits in
-// which register as long as both operands agree:
-//   S = Q K^T: lane (g, t) takes 16-byte chunks of key g (chunks 2 t, 2 t + 1),
-//     4 bytes per k-step; Q's fragments use the same columns.
-//   O = P V:  lane (g, t) takes chunk g of values 2 t, 2 t + 1, 2 t + 8,
-//     2 t + 9; byte j of each is column 16 g + j, product n-tile j.
-template <int D, bool I8>
-__global__ void __launch_bounds__(kWarps * 32)
+// in registers, with the tokens (then the dimensions) as the 16 rows, so that a
+// byte is converted once for all of a warp's query rows and 8 of them cost half
+// of what 16 would.  A product's sum over k does not care which column sits in
+// which register as long as both operands agree, nor does the order of rows:
+//   S^T = K Q^T: lane (g, t) takes chunks 2 t, 2 t + 1 (16 bytes each) of keys g
+//     and g + 8, 4 bytes per k-step; Q's fragments use the same columns.
+//   O^T = V^T P^T: lane (g, t) takes chunk g of values 2 t, 2 t + 1, 2 t + 8,
+//     2 t + 9; bytes 2 j and 2 j + 1 of each are rows g and g + 8 of tile j.
+//     P^T's fragments are S^T's, transposed 8 x 8 by movmatrix.
+template <int D, bool I8, int NR, bool SHARE>
+__global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads)
     cache_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap) {
-  constexpr int KST = D / 16;              // k-steps of S
-  constexpr int NT = D / 8;                // n-tiles of O
-  constexpr int CH = D / 64;               // 16-byte chunks of a key per lane
-  constexpr int kBox = kStep * D;          // bytes of a step's keys (or values)
+  using Sh = AttnShape<D, NR, SHARE>;
+  constexpr int KST = D / 16;      // k-steps of S^T
+  constexpr int MT = D / 16;       // row tiles of O^T
+  constexpr int CH = D / 64;       // 16-byte chunks of a key per lane
+  constexpr int NS = Sh::kStages;
+  constexpr int kBox = Sh::kBox;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kWarps][kStages];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ __align__(8) uint64_t full[Sh::kRings][NS], empty[NS];
+  __shared__ float s_m[kWarps][8 * NR], s_l[kWarps][8 * NR];
   __shared__ uint32_t s_last;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % (unsigned)p.splits);
@@ -316,49 +349,69 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (!sequence(p.s, b, p.status, row0, fresh, len)) return;
   const int G = p.group;
   const int64_t total = (int64_t)fresh * G;  // query rows of the sequence and head
-  const int64_t r0 = (int64_t)qt * kRows;
-  if (r0 >= total) return;
-  const int nrows = (int)min((int64_t)kRows, total - r0);
-  const int i0 = (int)(r0 / G), i1 = (int)((r0 + nrows - 1) / G);  // first, last new token
-
-  // visible tokens: [0, sink) and [lo, hi); a query at place q sees t <= q
+  const int64_t u0 = (int64_t)qt * Sh::kRows;
+  if (u0 >= total) return;
+  const int urows = (int)min((int64_t)Sh::kRows, total - u0);
   const int first = len - fresh;
-  const int hi = len == 0 ? 0 : first + i1 + 1;
-  const int hi_min = first + i0 + 1;
-  const int lo = p.window ? max(0, first + i0 - p.window + 1) : 0;
-  const int lo_max = p.window ? first + i1 - p.window + 1 : 0;
-  int na = p.window ? (min(p.sinks, hi) + kStep - 1) / kStep : 0;  // steps of the sinks
-  int nb0 = lo / kStep;
-  if (nb0 <= na) na = nb0 = 0;
-  const int nsteps = hi == 0 ? 0 : na + (hi + kStep - 1) / kStep - nb0;
+
+  // the unit's visible tokens: [0, sinks) and [lo, hi); a query at place q sees t <= q
+  int na, nb0, nsteps;
+  {
+    const int i0 = (int)(u0 / G), i1 = (int)((u0 + urows - 1) / G);
+    const int uhi = len == 0 ? 0 : first + i1 + 1;
+    const int ulo = p.window ? max(0, first + i0 - p.window + 1) : 0;
+    na = p.window ? (min(p.sinks, uhi) + kStep - 1) / kStep : 0;  // steps of the sinks
+    nb0 = ulo / kStep;
+    if (nb0 <= na) na = nb0 = 0;
+    nsteps = uhi == 0 ? 0 : na + (uhi + kStep - 1) / kStep - nb0;
+  }
   const int active = max(1, (nsteps + p.chunk - 1) / p.chunk);  // CTAs with work
   if (split >= active) return;
-  const int s_begin = split * p.chunk + warp, s_end = min(nsteps, (split + 1) * p.chunk);
-  const int mine = s_begin < s_end ? (s_end - s_begin + kWarps - 1) / kWarps : 0;
+  const int stride = SHARE ? 1 : kWarps;
+  const int s_begin = split * p.chunk + (SHARE ? 0 : warp);
+  const int s_end = min(nsteps, (split + 1) * p.chunk);
+  const int mine = s_begin < s_end ? (s_end - s_begin + stride - 1) / stride : 0;
   auto base_of = [&](int j) {  // first token of this warp's step j
-    const int s = s_begin + j * kWarps;
+    const int s = s_begin + j * stride;
     return (s < na ? s : s - na + nb0) * kStep;
   };
 
+  // this warp's query rows and what they see
+  const bool computes = !SHARE || warp < kWarps;
+  const int64_t r0 = u0 + (SHARE ? 8 * NR * warp : 0);
+  const int nrows = !computes ? 0 : (int)max((int64_t)0, min((int64_t)(8 * NR), total - r0));
+  const int i0 = nrows ? (int)(r0 / G) : 0, i1 = nrows ? (int)((r0 + nrows - 1) / G) : 0;
+  const int hi = len == 0 || !nrows ? 0 : first + i1 + 1;
+  const int hi_min = first + i0 + 1;
+  const int lo = p.window ? max(0, first + i0 - p.window + 1) : 0;
+  const int lo_max = p.window ? first + i1 - p.window + 1 : 0;
+
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *ring = smem + warp * (kStages * 2 * kBox);
+  const int ring_no = SHARE ? 0 : warp;
+  uint8_t *ring = smem + ring_no * Sh::kRing;
   const uint32_t ring32 = smem_u32(ring);
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&full[warp][s], 1);
+  if (SHARE ? tid == 0 : lane == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[ring_no][s], 1);
+      if (SHARE) mbar_init(&empty[s], kWarps);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  __syncwarp();
+  if (SHARE)
+    __syncthreads();
+  else
+    __syncwarp();
 
-  // pages and scales, 16 steps at a time: lane l holds step l / 2's page of
-  // tokens 16 (l & 1) .. (the same page twice where pages hold a step)
+  // pages, 16 steps at a time: lane l holds step l / 2's page of tokens
+  // 16 (l & 1) .. (the same page twice where pages hold a step)
   const int32_t *table = p.s.table + b * p.s.table_stride;
   auto load_ids = [&](int w0) {
     const int j = w0 + (lane >> 1);
     int id = 0;
     if (j < mine) {
-      const int tok = base_of(j) + 16 * (lane & 1);
-      if (tok < hi) {
-        id = __ldg(table + (tok >> p.s.page_shift));
+      const int64_t tok = base_of(j) + 16 * (lane & 1);
+      if (tok < len) {
+        id = ld_dep(table + (tok >> p.s.page_shift));
         if (id < 0 || id >= p.num_pages) {
           atomicOr(p.status, kStatusBadSeq);
           id = 0;
@@ -367,282 +420,355 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     return id;
   };
-  auto load_scales = [&](int id, float &ks, float &vs) {
-    ks = __ldg(p.k_scale + (int64_t)id * p.kv_heads + h);
-    vs = __ldg(p.v_scale + (int64_t)id * p.kv_heads + h);
-  };
-  int id_cur = load_ids(0), id_nxt = load_ids(16);
-  float ks_cur, vs_cur, ks_nxt, vs_nxt;
-  load_scales(id_cur, ks_cur, vs_cur);
-  load_scales(id_nxt, ks_nxt, vs_nxt);
-
   const int P = 1 << p.s.page_shift;
-  const int boxes = P >= kStep ? 1 : 2;
-  auto issue = [&](int j, int id0, int id1) {  // lane 0: step j's boxes into its slot
-    const int s = j % kStages;
+  auto issue = [&](int j, int id0, int id1) {  // one lane: step j's boxes into its slot
+    const int s = j % NS;
     const uint32_t dst = ring32 + s * (2 * kBox);
-    const int tok = base_of(j);
-    const int place = tok & (P - 1);
-    mbar_arrive_expect_tx(&full[warp][s], 2 * kBox);
-    tma_load_4d(dst, &kmap, 0, place, h, id0, &full[warp][s]);
-    tma_load_4d(dst + kBox, &vmap, 0, place, h, id0, &full[warp][s]);
-    if (boxes == 2) {
-      tma_load_4d(dst + kBox / 2, &kmap, 0, 0, h, id1, &full[warp][s]);
-      tma_load_4d(dst + kBox + kBox / 2, &vmap, 0, 0, h, id1, &full[warp][s]);
+    const int place = base_of(j) & (P - 1);
+    uint64_t *bar = &full[ring_no][s];
+    mbar_arrive_expect_tx(bar, 2 * kBox);
+    tma_load_4d(dst, &kmap, 0, place, h, id0, bar);
+    tma_load_4d(dst + kBox, &vmap, 0, place, h, id0, bar);
+    if (P < kStep) {
+      tma_load_4d(dst + kBox / 2, &kmap, 0, 0, h, id1, bar);
+      tma_load_4d(dst + kBox + kBox / 2, &vmap, 0, 0, h, id1, bar);
     }
   };
-#pragma unroll
-  for (int j = 0; j < kStages; ++j) {
-    const int a = __shfl_sync(0xFFFFFFFFu, id_cur, 2 * j);
-    const int c = __shfl_sync(0xFFFFFFFFu, id_cur, 2 * j + 1);
-    if (j < mine && lane == 0) issue(j, a, c);
+
+  if (SHARE && warp == kWarps) {
+    // the warp that fills the shared ring
+    int ids = 0;
+    bool ok = true;
+    for (int j = 0; j < mine && ok; ++j) {
+      if ((j & 15) == 0) ids = load_ids(j);
+      const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j & 15));
+      const int id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (j & 15) + 1);
+      if (j >= NS) ok = mbar_wait(&empty[j % NS], ((uint32_t)(j / NS) & 1u) ^ 1u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok && lane == 0) issue(j, id0, id1);
+    }
+    if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
   }
 
-  // Q: rows g and g + 8, each times a power of two that brings its largest
-  // value to [128, 256), so that bf16's 8 bits survive the change to fp16
-  uint32_t qf[KST][4];
-  float qm[2];
-  int bound_hi[2], bound_lo[2];
+  float o[MT][NR][4];
+  float m[NR][2], l[NR][2];
+  if (computes) {
+    auto load_scales = [&](int id, float &ks, float &vs) {
+      ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
+      vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
+    };
+    int id_cur = load_ids(0), id_nxt = load_ids(16);
+    float ks_cur, vs_cur, ks_nxt, vs_nxt;
+    load_scales(id_cur, ks_cur, vs_cur);
+    load_scales(id_nxt, ks_nxt, vs_nxt);
+    if constexpr (!SHARE) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int rr = g + 8 * r;
-    const bool live = rr < nrows;
-    const int64_t row = r0 + (live ? rr : 0);
-    const int i = (int)(row / G), hd = h * G + (int)(row % G);
-    bound_hi[r] = live && len > 0 ? first + i + 1 : 0;
-    bound_lo[r] = p.window ? first + i - p.window + 1 : 0;
-    const uint16_t *src = p.Q + (row0 + i) * p.ldq + hd * p.hsq;
-    uint32_t w[CH][8];
-    uint32_t a = 0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const uint4 x = ld_keep16(src + (CH * t + c) * 16), y = ld_keep16(src + (CH * t + c) * 16 + 8);
-      w[c][0] = x.x; w[c][1] = x.y; w[c][2] = x.z; w[c][3] = x.w;
-      w[c][4] = y.x; w[c][5] = y.y; w[c][6] = y.z; w[c][7] = y.w;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        a = max(a, max((w[c][e] & 0x7FFFu) >> 7, (w[c][e] >> 23) & 0xFFu));
-    }
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-    a = max(a, 8u);  // exponent field of the row's largest value
-    const float f = __uint_as_float((261u - a) << 23);
-    qm[r] = p.qmul * __uint_as_float((a - 7u) << 23);  // 2^(a - 134)
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __half2 v = live ? __floats2half2_rn(bf16_lo(w[c][e]) * f, bf16_hi(w[c][e]) * f)
-                               : __float2half2_rn(0.0f);
-        qf[c * 4 + e / 2][2 * (e & 1) + r] = *reinterpret_cast<const uint32_t *>(&v);
+      for (int j = 0; j < NS; ++j) {
+        const int a = __shfl_sync(0xFFFFFFFFu, id_cur, 2 * j);
+        const int c = __shfl_sync(0xFFFFFFFFu, id_cur, 2 * j + 1);
+        if (j < mine && lane == 0) issue(j, a, c);
       }
-  }
-
-  float o[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[n][c] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-
-  for (int j = 0; j < mine; ++j) {
-    if ((j & 15) == 0 && j) {
-      id_cur = id_nxt;
-      ks_cur = ks_nxt;
-      vs_cur = vs_nxt;
-      id_nxt = load_ids(j + 16);
-      load_scales(id_nxt, ks_nxt, vs_nxt);
-    }
-    const int src = 2 * (j & 15);
-    const float ks0 = __shfl_sync(0xFFFFFFFFu, ks_cur, src);
-    const float ks1 = __shfl_sync(0xFFFFFFFFu, ks_cur, src + 1);
-    const float vs0 = __shfl_sync(0xFFFFFFFFu, vs_cur, src);
-    const float vs1 = __shfl_sync(0xFFFFFFFFu, vs_cur, src + 1);
-    const int slot = j % kStages;
-    const uint32_t kb = ring32 + slot * (2 * kBox), vb = kb + kBox;
-    const int base = base_of(j);
-    if (!mbar_wait(&full[warp][slot], (uint32_t)(j / kStages) & 1u)) {
-      if (lane == 0) atomicOr(p.status, kStatusTimeout);
-      // the copies behind it may still land
-      for (int q = j + 1; q < min(j + kStages, mine); ++q)
-        mbar_wait(&full[warp][q % kStages], (uint32_t)(q / kStages) & 1u);
-      break;
     }
 
-    float s[4][4];
+    // Q: row g of each tile, times a power of two that brings its largest value
+    // to [128, 256), so that bf16's 8 bits survive the change to fp16
+    uint32_t qf[NR][KST][2];
+    float qm[NR][2];                      // of rows 2 t and 2 t + 1: softmax scale and that power
+    int bound_hi[NR][2], bound_lo[NR][2];  // what those rows see
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[n][c] = 0.0f;
-      const int tok = n * 8 + g;
+    for (int n = 0; n < NR; ++n) {
+      const bool live = 8 * n + g < nrows;
+      const int64_t row = live ? r0 + 8 * n + g : u0;
+      const int i = (int)(row / G), hd = h * G + (int)(row % G);
+      const uint16_t *src = p.Q + (row0 + i) * p.ldq + hd * p.hsq;
+      uint32_t w[CH][8];
+      uint32_t a = 0;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const uint4 w = lds16(kb + swz<D>(tok, CH * t + c));
-        const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
+        const uint4 x = ld_dep16(src + (CH * t + c) * 16), y = ld_dep16(src + (CH * t + c) * 16 + 8);
+        w[c][0] = x.x; w[c][1] = x.y; w[c][2] = x.z; w[c][3] = x.w;
+        w[c][4] = y.x; w[c][5] = y.y; w[c][6] = y.z; w[c][7] = y.w;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_f16(s[n], qf[c * 4 + e], to_f16x2<I8, 0>(wv[e]), to_f16x2<I8, 1>(wv[e]));
+        for (int e = 0; e < 8; ++e)
+          a = max(a, max((w[c][e] & 0x7FFFu) >> 7, (w[c][e] >> 23) & 0xFFu));
       }
-    }
-
-    // t = s + log2(vs): P then carries the page's value scale, and the running
-    // maximum keeps it within fp16
-    const float lv0 = __log2f(vs0), lv1 = __log2f(vs1);
+      a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+      a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+      a = max(a, 8u);  // exponent field of the row's largest value
+      const float f = __uint_as_float((261u - a) << 23);
+      const float back = p.qmul * __uint_as_float((a - 7u) << 23);  // 2^(a - 134)
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        s[n][c] = fmaf(s[n][c], (n < 2 ? ks0 : ks1) * qm[c >> 1], n < 2 ? lv0 : lv1);
-    // a step that some row does not see whole
-    const bool edge = base + kStep > hi_min || base < lo_max;
-    if (edge) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int tok = base + n * 8 + 2 * t + (c & 1);
-          const bool see = tok < bound_hi[c >> 1] && (tok >= bound_lo[c >> 1] || tok < p.sinks);
-          if (!see) s[n][c] = -INFINITY;
+        for (int e = 0; e < 8; ++e) {
+          const __half2 v = live ? __floats2half2_rn(bf16_lo(w[c][e]) * f, bf16_hi(w[c][e]) * f)
+                                 : __float2half2_rn(0.0f);
+          qf[n][c * 4 + e / 2][e & 1] = *reinterpret_cast<const uint32_t *>(&v);
         }
-    }
-    float corr[2], ref[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float v = m[r];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) v = fmaxf(v, fmaxf(s[n][2 * r], s[n][2 * r + 1]));
-      v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
-      v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
-      const float safe = v == -INFINITY ? 0.0f : v;
-      corr[r] = ex2(m[r] - safe);
-      ref[r] = safe - kLift;
-      m[r] = v;
-    }
-    const float iv0 = __fdividef(1.0f, vs0), iv1 = __fdividef(1.0f, vs1);
-    uint32_t pf[2][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float a = ex2(s[n][2 * r] - ref[r]), c = ex2(s[n][2 * r + 1] - ref[r]);
-        if (n < 2)
-          sum0 += a + c;
-        else
-          sum1 += a + c;
-        const __half2 hp = __floats2half2_rn(a, c);
-        pf[n >> 1][2 * (n & 1) + r] = *reinterpret_cast<const uint32_t *>(&hp);
-      }
-      l[r] = fmaf(l[r], corr[r], fmaf(sum0, iv0, sum1 * iv1));
-    }
-    if (__any_sync(0xFFFFFFFFu, corr[0] != 1.0f || corr[1] != 1.0f)) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        o[n][0] *= corr[0];
-        o[n][1] *= corr[0];
-        o[n][2] *= corr[1];
-        o[n][3] *= corr[1];
+      for (int c = 0; c < 2; ++c) {
+        qm[n][c] = __shfl_sync(0xFFFFFFFFu, back, 4 * (2 * t + c));
+        const int rr = 8 * n + 2 * t + c;
+        const int ii = (int)((r0 + rr) / G);
+        bound_hi[n][c] = rr < nrows && len > 0 ? first + ii + 1 : 0;
+        bound_lo[n][c] = p.window ? first + ii - p.window + 1 : 0;
+        m[n][c] = -INFINITY;
+        l[n][c] = 0.0f;
       }
     }
+#pragma unroll
+    for (int k = 0; k < MT; ++k)
+#pragma unroll
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[k][n][c] = 0.0f;
 
+    for (int j = 0; j < mine; ++j) {
+      if ((j & 15) == 0 && j) {
+        id_cur = id_nxt;
+        ks_cur = ks_nxt;
+        vs_cur = vs_nxt;
+        id_nxt = load_ids(j + 16);
+        load_scales(id_nxt, ks_nxt, vs_nxt);
+      }
+      const int src = 2 * (j & 15);
+      float ks[2], vs[2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      uint32_t w[4][D / 32];  // values 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+      for (int i = 0; i < 2; ++i) {
+        ks[i] = __shfl_sync(0xFFFFFFFFu, ks_cur, src + i);
+        vs[i] = __shfl_sync(0xFFFFFFFFu, vs_cur, src + i);
+      }
+      const int slot = j % NS;
+      const uint32_t kb = ring32 + slot * (2 * kBox), vb = kb + kBox;
+      const int base = base_of(j);
+      if (!mbar_wait(&full[ring_no][slot], (uint32_t)(j / NS) & 1u)) {
+        if (lane == 0) atomicOr(p.status, kStatusTimeout);
+        // the copies behind it may still land
+        for (int q = j + 1; q < min(j + NS, mine); ++q)
+          mbar_wait(&full[ring_no][q % NS], (uint32_t)(q / NS) & 1u);
+        break;
+      }
+      // (shared steps may lie outside what this warp's rows see)
+      if (!SHARE || (base < hi && (base + kStep > lo || base < p.sinks))) {
+        float s[2][NR][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int tok = kk * 16 + 2 * t + (e & 1) + 8 * (e >> 1);
-        if constexpr (D == 128) {
-          const uint4 x = lds16(vb + swz<D>(tok, g));
-          w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
-        } else {
-          const uint2 x = lds8(vb + swz<D>(tok, g >> 1) + 8 * (g & 1));
-          w[e][0] = x.x; w[e][1] = x.y;
-        }
-        if (edge) {  // what lies in tokens that no row sees must not count
-          const int at = base + tok;
-          if (!(at < hi && (at >= lo || at < p.sinks))) {
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) w[e][q] = 0;
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[i][n][c] = 0.0f;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const uint4 x = lds16(kb + swz<D>(16 * i + g, CH * t + c));
+            const uint4 y = lds16(kb + swz<D>(16 * i + 8 + g, CH * t + c));
+            const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t a[4] = {to_f16x2<I8, 0>(xv[e]), to_f16x2<I8, 0>(yv[e]),
+                                     to_f16x2<I8, 1>(xv[e]), to_f16x2<I8, 1>(yv[e])};
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                mma_f16(s[i][n], a, qf[n][c * 4 + e][0], qf[n][c * 4 + e][1]);
+            }
           }
         }
-      }
-#pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        const uint32_t a01 = __byte_perm(w[0][q], w[1][q], 0x5140);
-        const uint32_t a23 = __byte_perm(w[0][q], w[1][q], 0x7362);
-        const uint32_t c01 = __byte_perm(w[2][q], w[3][q], 0x5140);
-        const uint32_t c23 = __byte_perm(w[2][q], w[3][q], 0x7362);
-        mma_f16(o[4 * q + 0], pf[kk], to_f16x2<I8, 0>(a01), to_f16x2<I8, 0>(c01));
-        mma_f16(o[4 * q + 1], pf[kk], to_f16x2<I8, 1>(a01), to_f16x2<I8, 1>(c01));
-        mma_f16(o[4 * q + 2], pf[kk], to_f16x2<I8, 0>(a23), to_f16x2<I8, 0>(c23));
-        mma_f16(o[4 * q + 3], pf[kk], to_f16x2<I8, 1>(a23), to_f16x2<I8, 1>(c23));
-      }
-    }
 
-    // every lane has read the slot: its next step may overwrite it
-    __syncwarp();
-    const int jn = j + kStages;
-    if (jn < mine) {
-      const int sl = 2 * (jn & 15);
-      const bool same = (jn >> 4) == (j >> 4);
-      const int a0 = __shfl_sync(0xFFFFFFFFu, id_cur, sl), a1 = __shfl_sync(0xFFFFFFFFu, id_cur, sl + 1);
-      const int c0 = __shfl_sync(0xFFFFFFFFu, id_nxt, sl), c1 = __shfl_sync(0xFFFFFFFFu, id_nxt, sl + 1);
-      if (lane == 0) issue(jn, same ? a0 : c0, same ? a1 : c1);
-    }
-  }
+        // t = s + log2(vs): P then carries the page's value scale, and the
+        // running maximum keeps it within fp16
+        const bool edge = base + kStep > hi_min || base < lo_max;  // some row does not see it whole
+        uint32_t pf[2][NR][2];
+        float corr[NR][2];
+        bool moved = false;
+        float lv[2], iv[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lv[i] = __log2f(vs[i]);
+          iv[i] = __fdividef(1.0f, vs[i]);
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v = m[n][c];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float f = ks[i] * qm[n][c];
+#pragma unroll
+              for (int d = 0; d < 2; ++d) {  // tokens g and g + 8
+                float &x = s[i][n][2 * d + c];
+                x = fmaf(x, f, lv[i]);
+                if (edge) {
+                  const int tok = base + 16 * i + 8 * d + g;
+                  if (!(tok < bound_hi[n][c] && (tok >= bound_lo[n][c] || tok < p.sinks)))
+                    x = -INFINITY;
+                }
+                v = fmaxf(v, x);
+              }
+            }
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+            const float safe = v == -INFINITY ? 0.0f : v;
+            corr[n][c] = ex2(m[n][c] - safe);
+            moved |= corr[n][c] != 1.0f;
+            m[n][c] = v;
+            const float ref = safe - kLift;
+            float sum[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s[i][n][c] = ex2(s[i][n][c] - ref);
+              s[i][n][2 + c] = ex2(s[i][n][2 + c] - ref);
+              sum[i] = s[i][n][c] + s[i][n][2 + c];
+            }
+            l[n][c] = fmaf(l[n][c], corr[n][c], fmaf(sum[0], iv[0], sum[1] * iv[1]));
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const __half2 hp = __floats2half2_rn(s[i][n][2 * d], s[i][n][2 * d + 1]);
+              pf[i][n][d] = movmatrix(*reinterpret_cast<const uint32_t *>(&hp));
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+          for (int k = 0; k < MT; ++k)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              o[k][n][0] *= corr[n][0];
+              o[k][n][1] *= corr[n][1];
+              o[k][n][2] *= corr[n][0];
+              o[k][n][3] *= corr[n][1];
+            }
+        }
 
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-  }
-  // the warp's rows into its ring's first slots (all its copies have landed)
-  float *wo = reinterpret_cast<float *>(ring);  // [16][D]
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[4][D / 32];  // values 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+          for (int e = 0; e < 4; ++e) {
+            const int tok = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
+            if constexpr (D == 128) {
+              const uint4 x = lds16(vb + swz<D>(tok, g));
+              w[e][0] = x.x; w[e][1] = x.y; w[e][2] = x.z; w[e][3] = x.w;
+            } else {
+              const uint2 x = lds8(vb + swz<D>(tok, g >> 1) + 8 * (g & 1));
+              w[e][0] = x.x; w[e][1] = x.y;
+            }
+            if (edge) {  // what lies in tokens that no row sees must not count
+              const int at = base + tok;
+              if (!(at < hi && (at >= lo || at < p.sinks))) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      wo[(g + 8 * (c >> 1)) * D + (D / 8) * (2 * t + (c & 1)) + n] = o[n][c];
-  if (t == 0) {
+                for (int q = 0; q < D / 32; ++q) w[e][q] = 0;
+              }
+            }
+          }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      s_m[warp][g + 8 * r] = m[r];
-      s_l[warp][g + 8 * r] = l[r];
+          for (int q = 0; q < D / 32; ++q)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {  // bytes 2 z, 2 z + 1 of word q: tile 2 q + z
+              const uint32_t x = __byte_perm(w[0][q], w[1][q], z ? 0x7362 : 0x5140);
+              const uint32_t y = __byte_perm(w[2][q], w[3][q], z ? 0x7362 : 0x5140);
+              const uint32_t a[4] = {to_f16x2<I8, 0>(x), to_f16x2<I8, 1>(x), to_f16x2<I8, 0>(y),
+                                     to_f16x2<I8, 1>(y)};
+#pragma unroll
+              for (int n = 0; n < NR; ++n) mma_f16(o[2 * q + z][n], a, pf[i][n][0], pf[i][n][1]);
+            }
+        }
+      }
+
+      // every lane has read the slot: its next step may overwrite it
+      __syncwarp();
+      if constexpr (SHARE) {
+        if (lane == 0) mbar_arrive(&empty[slot]);
+      } else {
+        const int jn = j + NS;
+        if (jn < mine) {
+          const bool same = (jn >> 4) == (j >> 4);
+          const int from = same ? id_cur : id_nxt;
+          const int a = __shfl_sync(0xFFFFFFFFu, from, 2 * (jn & 15));
+          const int c = __shfl_sync(0xFFFFFFFFu, from, 2 * (jn & 15) + 1);
+          if (lane == 0) issue(jn, a, c);
+        }
+      }
     }
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 4; x <= 16; x *= 2) l[n][c] += __shfl_xor_sync(0xFFFFFFFFu, l[n][c], x);
+  }
+  // a shared ring is free once every warp has left it; a warp's own is already
+  if (SHARE) __syncthreads();
+  if (computes) {
+    float *wo = reinterpret_cast<float *>(smem + warp * Sh::kWarpOut);  // [8 NR][kPitch]
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        // dimensions (D / 8) g .. of row 2 t + c
+        float *to = wo + (8 * n + 2 * t + c) * Sh::kPitch + (D / 8) * g;
+#pragma unroll
+        for (int k = 0; k < MT; k += 2)
+          *reinterpret_cast<float4 *>(to + 2 * k) =
+              make_float4(o[k][n][c], o[k][n][2 + c], o[k + 1][n][c], o[k + 1][n][2 + c]);
+        if (g == 0) {
+          s_m[warp][8 * n + 2 * t + c] = m[n][c];
+          s_l[warp][8 * n + 2 * t + c] = l[n][c];
+        }
+      }
   }
   __syncthreads();
 
-  constexpr int kPart = kRows * D + 2 * kRows;  // floats of one CTA's partial result
   const bool alone = active == 1;
-  float *mypart = alone ? nullptr : p.part + ((int64_t)unit * p.splits + split) * kPart;
-  auto write_out = [&](int row, int d, float num, float den, float mx) {
-    const int64_t rr = r0 + row;
+  float *mypart = alone ? nullptr : p.part + ((int64_t)unit * p.splits + split) * Sh::kPart;
+  // four dimensions of a row: the result, or this CTA's part of it
+  auto write_out = [&](int row, int d, float4 num, float den, float mx) {
+    const int64_t rr = u0 + row;
     const int i = (int)(rr / G), hd = h * G + (int)(rr % G);
-    p.O[(row0 + i) * p.ldo + hd * p.hso + d] = f32_to_bf16_rne(den != 0.0f ? num / den : 0.0f);
+    const float r = den != 0.0f ? 1.0f / den : 0.0f;
+    *reinterpret_cast<uint2 *>(p.O + (row0 + i) * p.ldo + hd * p.hso + d) =
+        make_uint2(f32_to_bf16_rne(num.x * r) | ((uint32_t)f32_to_bf16_rne(num.y * r) << 16),
+                   f32_to_bf16_rne(num.z * r) | ((uint32_t)f32_to_bf16_rne(num.w * r) << 16));
     if (d == 0 && p.lse)
       p.lse[(row0 + i) * p.ldl + hd] =
           den != 0.0f ? (mx - kLift + log2f(den)) * 0.693147180559945309f : -INFINITY;
   };
-  for (int e = tid; e < nrows * D; e += kWarps * 32) {
-    const int row = e / D, d = e % D;
-    float mx = s_m[0][row];
+  auto add = [](float4 &a, float f, const float4 &x) {
+    a.x = fmaf(f, x.x, a.x);
+    a.y = fmaf(f, x.y, a.y);
+    a.z = fmaf(f, x.z, a.z);
+    a.w = fmaf(f, x.w, a.w);
+  };
+  for (int e = tid; e < urows * (D / 4); e += Sh::kThreads) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float den = 0.0f, mx;
+    if constexpr (SHARE) {
+      const int w = row / (8 * NR), r = row % (8 * NR);
+      mx = s_m[w][r];
+      den = s_l[w][r];
+      num = *reinterpret_cast<const float4 *>(smem + w * Sh::kWarpOut + (r * Sh::kPitch + d) * 4);
+    } else {
+      mx = s_m[0][row];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
-    const float safe = mx == -INFINITY ? 0.0f : mx;
-    float num = 0.0f, den = 0.0f;
+      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][row]);
+      const float safe = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(s_m[w][row] - safe);
-      num = fmaf(f, reinterpret_cast<const float *>(smem + w * (kStages * 2 * kBox))[row * D + d], num);
-      den = fmaf(f, s_l[w][row], den);
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w][row] - safe);
+        add(num, f, *reinterpret_cast<const float4 *>(smem + w * Sh::kWarpOut + (row * Sh::kPitch + d) * 4));
+        den = fmaf(f, s_l[w][row], den);
+      }
     }
     if (alone) {
-      write_out(row, d, num, den, safe);
+      write_out(row, d, num, den, mx);
     } else {
-      mypart[row * D + d] = num;
+      *reinterpret_cast<float4 *>(mypart + row * D + d) = num;
       if (d == 0) {
-        mypart[kRows * D + row] = mx;
-        mypart[kRows * D + kRows + row] = den;
+        mypart[Sh::kRows * D + row] = mx;
+        mypart[Sh::kRows * D + Sh::kRows + row] = den;
       }
     }
   }
@@ -657,20 +783,22 @@ __global__ void __launch_bounds__(kWarps * 32)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const float *up = p.part + (int64_t)unit * p.splits * kPart;
-  for (int e = tid; e < nrows * D; e += kWarps * 32) {
-    const int row = e / D, d = e % D;
+  const float *up = p.part + (int64_t)unit * p.splits * Sh::kPart;
+  for (int e = tid; e < urows * (D / 4); e += Sh::kThreads) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
     float mx = -INFINITY;
-    for (int s = 0; s < active; ++s) mx = fmaxf(mx, __ldcg(up + (int64_t)s * kPart + kRows * D + row));
+    for (int s = 0; s < active; ++s)
+      mx = fmaxf(mx, __ldcg(up + (int64_t)s * Sh::kPart + Sh::kRows * D + row));
     const float safe = mx == -INFINITY ? 0.0f : mx;
-    float num = 0.0f, den = 0.0f;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float den = 0.0f;
     for (int s = 0; s < active; ++s) {
-      const float *q = up + (int64_t)s * kPart;
-      const float f = ex2(__ldcg(q + kRows * D + row) - safe);
-      num = fmaf(f, __ldcg(q + row * D + d), num);
-      den = fmaf(f, __ldcg(q + kRows * D + kRows + row), den);
+      const float *q = up + (int64_t)s * Sh::kPart;
+      const float f = ex2(__ldcg(q + Sh::kRows * D + row) - safe);
+      add(num, f, __ldcg(reinterpret_cast<const float4 *>(q + row * D + d)));
+      den = fmaf(f, __ldcg(q + Sh::kRows * D + Sh::kRows + row), den);
     }
-    write_out(row, d, num, den, safe);
+    write_out(row, d, num, den, mx);
   }
 }
 
@@ -728,7 +856,7 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
 // time).  Only units that are split have tickets, which lie at a fixed place
 // whatever the call's shape, so that calls of different shapes can share a
 // workspace.
-constexpr int kMinChunk = 4, kMaxChunk = 32;
+constexpr int kMinChunk = kWarps, kMaxChunk = 32;
 constexpr int kTickets = 2048;
 void split_plan(int64_t units, int64_t tokens, int sms, int *splits, int *chunk) {
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;  // a range may start inside a step
@@ -742,11 +870,15 @@ void split_plan(int64_t units, int64_t tokens, int sms, int *splits, int *chunk)
   *splits = (int)((steps + c - 1) / c);
 }
 
+// Query rows (of one head and sequence) per unit: 8 or 16 in a CTA that splits
+// the tokens over its warps, else 64 in one whose warps have 16 each.
+int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 64; }
+
 int attn_units(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t heads, int64_t *units,
                int *qtiles) {
   if (batch < 1 || max_new < 1 || heads < 1 || heads % C->kv_heads != 0) return HYB_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_new * (heads / C->kv_heads);
-  const int64_t qt = (rows + kRows - 1) / kRows;
+  const int64_t qt = (rows + unit_rows(rows) - 1) / unit_rows(rows);
   *units = (int64_t)batch * C->kv_heads * qt;
   if (batch > 65535 || max_new > (1 << 24) || *units > (1 << 30)) return HYB_ERR_UNSUPPORTED;
   *qtiles = (int)qt;
@@ -755,8 +887,9 @@ int attn_units(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t heads
 
 // workspace: header, tickets, partial results
 constexpr size_t kPartOffset = kHeaderBytes + 4 * kTickets;
-size_t attn_bytes(const hyb_cache *C, int64_t units, int splits) {
-  return kPartOffset + (splits > 1 ? (size_t)units * splits * (kRows * C->head_dim + 2 * kRows) * 4 : 0);
+size_t attn_bytes(const hyb_cache *C, int64_t units, int rows, int splits) {
+  return kPartOffset +
+         (splits > 1 ? (size_t)units * splits * (rows * C->head_dim + 2 * rows) * 4 : 0);
 }
 
 int encode_pages(const hyb_cache *C, const uint8_t *base, CUtensorMap *map) {
@@ -777,16 +910,25 @@ int encode_pages(const hyb_cache *C, const uint8_t *base, CUtensorMap *map) {
   return res == CUDA_SUCCESS ? HYB_OK : HYB_ERR_CUDA;
 }
 
-template <int D, bool I8>
-int launch_attention(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm,
-                     int64_t units, cudaStream_t st) {
-  const size_t dyn = (size_t)kWarps * kStages * 2 * kStep * D + 1024;
-  if (cudaFuncSetAttribute(cache_attention_kernel<D, I8>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn) != cudaSuccess)
+template <int D, bool I8, int NR, bool SHARE>
+int launch_shape(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int64_t units,
+                 cudaStream_t st) {
+  using Sh = AttnShape<D, NR, SHARE>;
+  const int dyn = Sh::kBytes + 1024;
+  if (cudaFuncSetAttribute(cache_attention_kernel<D, I8, NR, SHARE>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
     return HYB_ERR_CUDA;
   if (units * p.splits > INT32_MAX) return HYB_ERR_UNSUPPORTED;
-  cache_attention_kernel<D, I8><<<(unsigned)(units * p.splits), kWarps * 32, dyn, st>>>(p, km, vm);
-  return cudaGetLastError() == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
+  return launch_dependent(cache_attention_kernel<D, I8, NR, SHARE>,
+                          dim3((unsigned)(units * p.splits)), Sh::kThreads, dyn, 1, st, p, km, vm);
+}
+
+template <int D, bool I8>
+int launch_attention(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm,
+                     int64_t units, int rows, cudaStream_t st) {
+  return rows == 8    ? launch_shape<D, I8, 1, false>(p, km, vm, units, st)
+         : rows == 16 ? launch_shape<D, I8, 2, false>(p, km, vm, units, st)
+                      : launch_shape<D, I8, 2, true>(p, km, vm, units, st);
 }
 
 }  // namespace
@@ -832,18 +974,11 @@ int hyb_cache_append(const hyb_cache *C, const hyb_sequences *S, const uint16_t 
   const int64_t touched = ((int64_t)S->max_new + C->page_size - 2) / C->page_size + 1;
   const dim3 grid((unsigned)(2 * touched), (unsigned)C->kv_heads, (unsigned)S->batch);
   cudaStream_t st = (cudaStream_t)stream;
-  if (C->head_dim == 128) {
-    if (C->type == HYB_I8)
-      cache_append_kernel<128, true><<<grid, 128, 0, st>>>(p);
-    else
-      cache_append_kernel<128, false><<<grid, 128, 0, st>>>(p);
-  } else {
-    if (C->type == HYB_I8)
-      cache_append_kernel<64, true><<<grid, 128, 0, st>>>(p);
-    else
-      cache_append_kernel<64, false><<<grid, 128, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
+  const bool i8 = C->type == HYB_I8;
+  return launch_dependent(C->head_dim == 128
+                              ? (i8 ? cache_append_kernel<128, true> : cache_append_kernel<128, false>)
+                              : (i8 ? cache_append_kernel<64, true> : cache_append_kernel<64, false>),
+                          grid, 128, 0, 1, st, p);
 }
 
 size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch, int32_t max_new,
@@ -854,7 +989,7 @@ size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch, in
   if (attn_units(C, batch, max_new, heads, &units, &qtiles) != HYB_OK) return 0;
   if (device_sm_count(&sms) != HYB_OK) return 0;
   split_plan(units, (int64_t)max_pages * C->page_size, sms, &splits, &chunk);
-  return attn_bytes(C, units, splits);
+  return attn_bytes(C, units, unit_rows((int64_t)max_new * (heads / C->kv_heads)), splits);
 }
 
 int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16_t *Q, int64_t ldq,
@@ -889,7 +1024,7 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   const int64_t all = (int64_t)S->max_pages * C->page_size;
   int64_t tokens = all;
   if (window) {
-    const int64_t span = (int64_t)window + kRows + (int64_t)sinks + 2 * kStep;
+    const int64_t span = (int64_t)window + 64 + (int64_t)sinks + 2 * kStep;
     if (span < tokens) tokens = span;
   }
   int full_splits, full_chunk;
@@ -926,9 +1061,10 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   if (rc == HYB_OK) rc = encode_pages(C, C->v, &vm);
   if (rc != HYB_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
+  const int rows = unit_rows((int64_t)S->max_new * p.group);
   if (C->head_dim == 128)
-    return C->type == HYB_I8 ? launch_attention<128, true>(p, km, vm, units, st)
-                             : launch_attention<128, false>(p, km, vm, units, st);
-  return C->type == HYB_I8 ? launch_attention<64, true>(p, km, vm, units, st)
-                           : launch_attention<64, false>(p, km, vm, units, st);
+    return C->type == HYB_I8 ? launch_attention<128, true>(p, km, vm, units, rows, st)
+                             : launch_attention<128, false>(p, km, vm, units, rows, st);
+  return C->type == HYB_I8 ? launch_attention<64, true>(p, km, vm, units, rows, st)
+                           : launch_attention<64, false>(p, km, vm, units, rows, st);
 }

@@ -41,12 +41,14 @@ __device__ __forceinline__ void load8(const void *X, int64_t off, int left, bool
                                       float (&v)[8]) {
   if (left >= 8 && vec) {
     if constexpr (F32) {
-      const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(X) + off);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const float *p = static_cast<const float *>(X) + off;
+      const uint4 a = ld_dep16(p), b = ld_dep16(p + 4);
+      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+      v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+      v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
     } else {
-      const uint4 r = ld_keep16(static_cast<const uint16_t *>(X) + off);
+      const uint4 r = ld_dep16(static_cast<const uint16_t *>(X) + off);
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -60,9 +62,9 @@ __device__ __forceinline__ void load8(const void *X, int64_t off, int left, bool
       v[i] = 0.0f;
       if (i < left) {
         if constexpr (F32)
-          v[i] = static_cast<const float *>(X)[off + i];
+          v[i] = ld_dep(static_cast<const float *>(X) + off + i);
         else
-          v[i] = __uint_as_float((uint32_t) static_cast<const uint16_t *>(X)[off + i] << 16);
+          v[i] = __uint_as_float((uint32_t) static_cast<const volatile uint16_t *>(X)[off + i] << 16);
       }
     }
   }
@@ -101,25 +103,5 @@ int fp8_decode(const Fp8Params &p, cudaStream_t st);
 // or e4m3.
 bool fp8_is_small(int64_t m, int64_t n, int64_t k);
 int fp8_small(const Fp8Params &p, cudaStream_t st);
-
-// A launch as a programmatic dependent, in clusters of C CTAs along x.
-template <typename... P, typename... A>
-int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, int C,
-                     cudaStream_t st, const A &...args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)C;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = C > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
-}
 
 }  // namespace hyb

@@ -14,8 +14,8 @@
 //     one register and W's scale one per 128 columns: a block costs one FMA per
 //     value and no other scale traffic.
 //   * warp 0 moves operand blocks with TMA (128-byte rows in the 128-byte
-//     swizzle: one block of k is one swizzle row), warp 1 issues the MMAs, warps
-//     2-9 (two per lane quarter, half of the columns each) scale and add.
+//     swizzle: one block of k is one swizzle row), warp 1 issues the MMAs, the
+//     last 8 (two per lane quarter, half of the columns each) scale and add.
 //   * Where the tiles alone do not fill the GPU, a cluster of CTAs splits k; its
 //     partial sums meet in distributed shared memory in a fixed order.
 #include "hyb_fp8.cuh"
@@ -29,7 +29,6 @@ namespace hyb {
 namespace {
 
 constexpr int kTok = 128;       // tokens per CTA
-constexpr int kThreads = 320;   // producer, MMA, 8 epilogue warps
 
 template <int BN>
 struct Shape {
@@ -39,6 +38,11 @@ struct Shape {
   static constexpr int kCols = BN / 2;               // columns per epilogue thread
   static constexpr int kPitch = BN + 4;              // floats per row of the result in shared memory
   static constexpr int kTmem = 2 * BN;
+  static constexpr int kLoad = BN == 256 ? 32 : 16;  // columns per tensor-memory read
+  // producer, MMA (for BN = 256 a whole warpgroup, which hands its registers
+  // on), then 8 epilogue warps
+  static constexpr int kCtl = 2;
+  static constexpr int kThreads = 32 * (kCtl + 8);
   static_assert(kTok * kPitch * 4 <= kRing, "the result reuses the ring");
   static_assert(kStage % 1024 == 0, "swizzle alignment");
 };
@@ -53,25 +57,86 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
       : "memory");
 }
 
-// 16 columns of this thread's lane; the values are there after tmem_wait16
-__device__ __forceinline__ void tmem_issue16(uint32_t taddr, uint32_t (&r)[16]) {
+// N (16 or 32) columns of this thread's lane; the values are there after
+// tmem_wait
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_issue(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
+                 "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
+// acc += d * s on pairs of fp32
+__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  asm("{\n\t.reg .b64 d;\n\t"
+      "mov.b64 d, {%1, %2};\n\t"
+      "fma.rn.f32x2 %0, d, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s));
+}
+__device__ __forceinline__ uint64_t twice(float s) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(s)));
+  return r;
+}
+
+// One block's products (COLS columns from taddr) times `scale` onto acc;
+// `freed` gets this thread's arrival once they have been read.  The next N
+// columns are on their way while N are added.
+template <int COLS, int N>
+__device__ __forceinline__ void scale_add(uint32_t taddr, float scale, uint64_t (&acc)[COLS / 2],
+                                          uint64_t *freed) {
+  const uint64_t s = twice(scale);
+  uint32_t d[2][N];
+  tmem_issue(taddr, d[0]);
+#pragma unroll
+  for (int c = 0; c < COLS / N; ++c) {
+    tmem_wait(d[c & 1]);
+    if (c + 1 < COLS / N) {
+      tmem_issue(taddr + N * (c + 1), d[(c + 1) & 1]);
+    } else {
+      tc_fence_before();
+      mbar_arrive(freed);
+    }
+#pragma unroll
+    for (int q = 0; q < N / 2; ++q)
+      fma2(acc[N / 2 * c + q], d[c & 1][2 * q], d[c & 1][2 * q + 1], s);
+  }
+}
+
 template <int BN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Shape<BN>::kThreads)
     fp8_gemm_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap xmap,
                     const __grid_constant__ CUtensorMap wmap) {
   using Sh = Shape<BN>;
@@ -112,6 +177,8 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+
+
 
   if (warp == 0) {
     if (lane == 0) {
@@ -155,48 +222,34 @@ __global__ void __launch_bounds__(kThreads)
       if (!ok) atomicOr(p.status, kStatusTimeout);
     }
     __syncwarp();
-  } else {
-    const int half = (warp - 2) >> 2;
+  } else if (warp >= Sh::kCtl) {
+    const int half = (warp - Sh::kCtl) >> 2;
     const int row = 32 * (warp & 3) + lane;  // this thread's token, its tensor-memory lane
     const uint32_t tbase = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(half * Sh::kCols);
-    float acc[Sh::kCols];
+    uint64_t acc[Sh::kCols / 2];  // pairs of fp32
 #pragma unroll
-    for (int c = 0; c < Sh::kCols; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < Sh::kCols / 2; ++c) acc[c] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float *sxp = p.sx + min(m0 + row, p.m - 1) * p.ldsx + b0;
     // the scale of this thread's columns (they lie in one block of 128 rows of W)
     const float *swp = p.sw + min(n0 + half * Sh::kCols, p.n - 1) / kBlk * p.ldsw + b0;
     float sx = 0.0f, sw = 0.0f;
     if (nb > 0) {
-      sx = __ldg(sxp);
-      sw = __ldg(swp);
+      sx = ld_dep(sxp);
+      sw = ld_dep(swp);
     }
     bool ok = true;
     for (int j = 0; j < nb; ++j) {
       const int buf = j & 1;
       const float s = sx * sw;
       if (j + 1 < nb) {
-        sx = __ldg(sxp + j + 1);
-        sw = __ldg(swp + j + 1);
+        sx = ld_dep(sxp + j + 1);
+        sw = ld_dep(swp + j + 1);
       }
       ok = ring_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u);
       if (!ok) break;
       tc_fence_after();
-      uint32_t d[2][16];
-      tmem_issue16(tbase + buf * BN, d[0]);
-#pragma unroll
-      for (int c = 0; c < Sh::kCols / 16; ++c) {
-        tmem_wait16(d[c & 1]);
-        if (c + 1 < Sh::kCols / 16) {
-          tmem_issue16(tbase + buf * BN + 16 * (c + 1), d[(c + 1) & 1]);
-        } else {
-          tc_fence_before();
-          mbar_arrive(&tempty[buf]);
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          acc[16 * c + q] = fmaf(__uint_as_float(d[c & 1][q]), s, acc[16 * c + q]);
-      }
+      scale_add<Sh::kCols, Sh::kLoad>(tbase + buf * BN, s, acc, &tempty[buf]);
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
     // every epilogue thread is past its last block: the MMAs have read the ring
@@ -204,7 +257,7 @@ __global__ void __launch_bounds__(kThreads)
     float *out = reinterpret_cast<float *>(smem) + row * Sh::kPitch + half * Sh::kCols;
 #pragma unroll
     for (int c = 0; c < Sh::kCols; c += 4)
-      *reinterpret_cast<float4 *>(out + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+      *reinterpret_cast<ulonglong2 *>(out + c) = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
   }
   tc_fence_before();
   __syncthreads();  // warps that wait here do not poll, as they would in the cluster's barrier
@@ -216,7 +269,7 @@ __global__ void __launch_bounds__(kThreads)
     const float *mine = reinterpret_cast<const float *>(smem);
     const int es = p.bf16_out ? 2 : 4;
     const bool vec = ((uintptr_t)p.Y % 16 == 0) && (p.ldy * es % 16 == 0);
-    for (int r = rank + C * warp; r < rows; r += C * (kThreads / 32)) {
+    for (int r = rank + C * warp; r < rows; r += C * (Sh::kThreads / 32)) {
       for (int c = lane * 8; c < BN; c += 256) {
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int q = 0; q < C; ++q) {
@@ -292,7 +345,7 @@ int launch_gemm(const Fp8Params &p, int C, cudaStream_t st) {
   if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            dyn) != cudaSuccess)
     return HYB_ERR_CUDA;
-  return launch_dependent(fp8_gemm_kernel<BN>, dim3((unsigned)(tiles * C), (unsigned)toks), kThreads, dyn, C, st, p,
+  return launch_dependent(fp8_gemm_kernel<BN>, dim3((unsigned)(tiles * C), (unsigned)toks), Sh::kThreads, dyn, C, st, p,
                           xmap, wmap);
 }
 
@@ -322,6 +375,7 @@ struct DecodeShape {
   static constexpr int kCols = BN / 2;
   static constexpr int kPitch = BN + 4;
   static constexpr int kTmem = 2 * BN;
+  static constexpr int kLoad = 16;
   static_assert(kDecodeTokens * kPitch * 4 <= kStage * kStages, "the result reuses the ring");
   static_assert(kStage % 1024 == 0, "swizzle alignment");
 };
@@ -418,52 +472,37 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     // scale and add: lane = token (lanes 0 .. 31 of tensor memory), half of the columns
     const int half = warp >> 2;
     const uint32_t tbase = tmem + (uint32_t)(half * Sh::kCols);
-    float acc[Sh::kCols];
+    uint64_t acc[Sh::kCols / 2];  // pairs of fp32
 #pragma unroll
-    for (int c = 0; c < Sh::kCols; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < Sh::kCols / 2; ++c) acc[c] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float *sxp = p.sx + min(lane, m - 1) * p.ldsx + b0;
     const float *swp = p.sw + min(n0 + half * Sh::kCols, p.n - 1) / kBlk * p.ldsw + b0;
     float sx = 0.0f, sw = 0.0f;
     if (nb > 0) {
-      sx = __ldg(sxp);
-      sw = __ldg(swp);
+      sx = ld_dep(sxp);
+      sw = ld_dep(swp);
     }
     bool ok = true;
     for (int j = 0; j < nb; ++j) {
       const int buf = j & 1;
       const float s = sx * sw;
       if (j + 1 < nb) {
-        sx = __ldg(sxp + j + 1);
-        sw = __ldg(swp + j + 1);
+        sx = ld_dep(sxp + j + 1);
+        sw = ld_dep(swp + j + 1);
       }
       ok = ring_wait(&tfull[buf], (uint32_t)(j >> 1) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t d[2][16];
-      tmem_issue16(tbase + buf * BN, d[0]);
-#pragma unroll
-      for (int c = 0; c < Sh::kCols / 16; ++c) {
-        tmem_wait16(d[c & 1]);
-        if (c + 1 < Sh::kCols / 16) {
-          tmem_issue16(tbase + buf * BN + 16 * (c + 1), d[(c + 1) & 1]);
-        } else {
-          tc_fence_before();
-          mbar_arrive(&tempty[buf]);
-        }
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          acc[16 * c + q] = fmaf(__uint_as_float(d[c & 1][q]), s, acc[16 * c + q]);
-      }
+      scale_add<Sh::kCols, Sh::kLoad>(tbase + buf * BN, s, acc, &tempty[buf]);
     }
     if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
     if (lane < m) {  // past the last block: the MMAs have read the ring
       float *out = reinterpret_cast<float *>(smem) + lane * Sh::kPitch + half * Sh::kCols;
 #pragma unroll
       for (int c = 0; c < Sh::kCols; c += 4)
-        *reinterpret_cast<float4 *>(out + c) =
-            make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+        *reinterpret_cast<ulonglong2 *>(out + c) = make_ulonglong2(acc[c / 2], acc[c / 2 + 1]);
     }
   }
   tc_fence_before();

@@ -69,12 +69,12 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_small_kernel(const Fp8Params 
         const int64_t row = row0 + 8 * h + g;
         w[u][h][q] = make_uint4(0, 0, 0, 0);
         if (row < p.n && col(u, q) < p.k)
-          w[u][h][q] = ld_stream16(p.W + row * p.ldw + col(u, q));
+          w[u][h][q] = ld_dep_stream16(p.W + row * p.ldw + col(u, q));
       }
   float sw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    sw[u] = b0 + u < kb ? __ldg(p.sw + row0 / kBlk * p.ldsw + b0 + u) : 0.0f;
+    sw[u] = b0 + u < kb ? ld_dep(p.sw + row0 / kBlk * p.ldsw + b0 + u) : 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool live = g < p.m;
   uint4 x[U][XW];
@@ -86,11 +86,11 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_small_kernel(const Fp8Params 
       const int64_t c = XBF16 ? col(u, q >> 1) + 8 * (q & 1) : col(u, q);
       x[u][q] = make_uint4(0, 0, 0, 0);
       if (live && c < p.k)
-        x[u][q] = XBF16 ? ld_keep16(static_cast<const uint16_t *>(p.X) + g * p.ldx + c)
-                        : ld_keep16(static_cast<const uint8_t *>(p.X) + g * p.ldx + c);
+        x[u][q] = XBF16 ? ld_dep16(static_cast<const uint16_t *>(p.X) + g * p.ldx + c)
+                        : ld_dep16(static_cast<const uint8_t *>(p.X) + g * p.ldx + c);
     }
     sx[u] = 0.0f;
-    if (!XBF16 && live && b0 + u < kb) sx[u] = __ldg(p.sx + g * p.ldsx + b0 + u);
+    if (!XBF16 && live && b0 + u < kb) sx[u] = ld_dep(p.sx + g * p.ldsx + b0 + u);
   }
 
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -96,6 +96,38 @@ __device__ __forceinline__ uint4 ld_keep16(const void *p) {
   return __ldg(reinterpret_cast<const uint4 *>(p));
 }
 
+// ---- loads behind griddepcontrol.wait ---------------------------------------
+// A kernel that starts while the one before it still runs must not read that
+// one's output through the read-only path: a line that an SM fetched before
+// the write stays in its L1 and would be read stale.  These are plain loads.
+__device__ __forceinline__ float ld_dep(const float *p) {
+  float r;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ int32_t ld_dep(const int32_t *p) {
+  int32_t r;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(r) : "l"(p) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint4 ld_dep16(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+// the same for a weight, which is read once
+__device__ __forceinline__ uint4 ld_dep_stream16(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 // ---- host helpers -----------------------------------------------------------
 int device_sm_count(int *out);  // cached per device
 
@@ -174,6 +206,26 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   return encode;
+}
+
+// A launch as a programmatic dependent, in clusters of C CTAs along x.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, int C,
+                     cudaStream_t st, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)C;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, (P)args...) == cudaSuccess ? HYB_OK : HYB_ERR_CUDA;
 }
 
 }  // namespace hyb
