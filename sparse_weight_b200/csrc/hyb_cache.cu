@@ -322,7 +322,7 @@ struct AttnShape {
 //     2 t + 9; bytes 2 j and 2 j + 1 of each are rows g and g + 8 of tile j.
 //     P^T's fragments are S^T's, transposed 8 x 8 by movmatrix.
 template <int D, bool I8, int NR, bool SHARE>
-__global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads)
+__global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3 : 2)
     cache_attention_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap) {
   using Sh = AttnShape<D, NR, SHARE>;
@@ -858,9 +858,9 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
 // workspace.
 constexpr int kMinChunk = kWarps, kMaxChunk = 32;
 constexpr int kTickets = 2048;
-void split_plan(int64_t units, int64_t tokens, int sms, int *splits, int *chunk) {
+void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, int *chunk) {
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;  // a range may start inside a step
-  const bool many = units >= 8ll * sms || units > kTickets;
+  const bool many = units >= (rows > 16 ? 2ll : 8ll) * sms || units > kTickets;
   const int64_t want = many ? 1 : (4ll * sms + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
   if (c < kMinChunk) c = kMinChunk;
@@ -988,8 +988,9 @@ size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch, in
   int qtiles, sms, splits, chunk;
   if (attn_units(C, batch, max_new, heads, &units, &qtiles) != HYB_OK) return 0;
   if (device_sm_count(&sms) != HYB_OK) return 0;
-  split_plan(units, (int64_t)max_pages * C->page_size, sms, &splits, &chunk);
-  return attn_bytes(C, units, unit_rows((int64_t)max_new * (heads / C->kv_heads)), splits);
+  const int rows = unit_rows((int64_t)max_new * (heads / C->kv_heads));
+  split_plan(units, rows, (int64_t)max_pages * C->page_size, sms, &splits, &chunk);
+  return attn_bytes(C, units, rows, splits);
 }
 
 int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16_t *Q, int64_t ldq,
@@ -1027,9 +1028,10 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
     const int64_t span = (int64_t)window + 64 + (int64_t)sinks + 2 * kStep;
     if (span < tokens) tokens = span;
   }
+  const int rows = unit_rows((int64_t)S->max_new * (heads / C->kv_heads));
   int full_splits, full_chunk;
-  split_plan(units, all, sms, &full_splits, &full_chunk);
-  split_plan(units, tokens, sms, &splits, &chunk);
+  split_plan(units, rows, all, sms, &full_splits, &full_chunk);
+  split_plan(units, rows, tokens, sms, &splits, &chunk);
   if (splits > full_splits) {  // never more than the workspace holds
     splits = full_splits;
     chunk = full_chunk;
@@ -1061,7 +1063,6 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   if (rc == HYB_OK) rc = encode_pages(C, C->v, &vm);
   if (rc != HYB_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  const int rows = unit_rows((int64_t)S->max_new * p.group);
   if (C->head_dim == 128)
     return C->type == HYB_I8 ? launch_attention<128, true>(p, km, vm, units, rows, st)
                              : launch_attention<128, false>(p, km, vm, units, rows, st);
