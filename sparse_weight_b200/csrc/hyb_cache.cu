@@ -6,44 +6,12 @@
 //   O[i]    = sum_t softmax_t(S[i]) (vs[page(t)] vq_t)
 //
 // causal, with an optional window and sinks.
-#include "hyb_internal.cuh"
-
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
+#include "hyb_cache.cuh"
 
 namespace hyb {
 namespace {
 
 constexpr int kMinExp = -40, kMaxExp = 60;  // exponents of a scale that the append writes
-
-struct SeqParams {
-  int batch, max_new;
-  int64_t rows;
-  const int32_t *lens, *off, *table;
-  int max_pages;
-  int64_t table_stride;
-  int page_shift;  // log2 of the page size
-};
-
-// Sequence b: its first row, its new tokens and its length; false (flagged)
-// where the caller's arrays contradict one another.
-__device__ __forceinline__ bool sequence(const SeqParams &s, int b, uint32_t *status,
-                                         int64_t &row0, int &fresh, int &len) {
-  len = ld_dep(s.lens + b);
-  bool ok = len >= 0 && (int64_t)len <= ((int64_t)s.max_pages << s.page_shift);
-  if (s.off) {
-    const int64_t o0 = ld_dep(s.off + b), o1 = ld_dep(s.off + b + 1);
-    ok &= o0 >= 0 && o0 <= o1 && o1 <= s.rows && o1 - o0 <= s.max_new;
-    row0 = o0;
-    fresh = (int)(o1 - o0);
-  } else {
-    row0 = (int64_t)b * s.max_new;
-    fresh = s.max_new;
-  }
-  ok &= len == 0 || len >= fresh;
-  if (!ok) atomicOr(status, kStatusBadSeq);
-  return ok;
-}
 
 // ---------------------------------------------------------------------------
 // append
@@ -198,40 +166,6 @@ constexpr int kWarps = 4;   // warps that compute
 // reach down to 2^-29 of the largest one and its steps to 2^-39
 constexpr float kLift = 15.0f;
 
-struct AttnParams {
-  SeqParams s;
-  const uint16_t *Q;
-  int64_t ldq, hsq;
-  uint16_t *O;
-  int64_t ldo, hso;
-  float *lse;
-  int64_t ldl;
-  const float *k_scale, *v_scale;
-  int num_pages, kv_heads, group;
-  float qmul;  // softmax_scale * log2(e)
-  int window, sinks;
-  int qtiles;  // units per sequence and head
-  int splits, chunk;  // CTAs per unit, steps of each
-  float *part;        // [unit][split]: O [16][D], mref [16], l [16]
-  uint32_t *tickets;  // [unit]
-  uint32_t *status;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                            int z, int w, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // D += A B, fp16 operands, fp32 accumulation
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
@@ -240,43 +174,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// two 8-bit values (the low or high half of w) as a pair of fp16, exactly
-template <bool I8, int HALF>
-__device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
-  uint32_t r;
-  if constexpr (I8) {
-    // 0x6400 | (q + 128) is 1024 + 128 + q in fp16
-    const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, HALF ? 0x4342 : 0x4140);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
-    r = *reinterpret_cast<const uint32_t *>(&x);
-  } else {
-    const uint16_t two = (uint16_t)(HALF ? w >> 16 : w);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-  }
-  return r;
-}
-
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-  return r;
-}
-
-// byte offset of 16-byte chunk c of row r in a box of D-byte rows, as the
-// tensor map's swizzle (128 or 64 bytes) stores it
-template <int D>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
-  return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
 // transpose of an 8 x 8 matrix of fp16 held by the warp
@@ -850,29 +747,34 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
   return HYB_OK;
 }
 
-// The split of a unit's steps: enough CTAs to fill the GPU a few times over,
-// none below 4 steps (one per warp) nor, unless the units alone fill it, above
-// 32 (1024 tokens: sequences of different lengths then end at about the same
-// time).  Only units that are split have tickets, which lie at a fixed place
-// whatever the call's shape, so that calls of different shapes can share a
-// workspace.
-constexpr int kMinChunk = kWarps, kMaxChunk = 32;
+// The split of a unit's steps: enough CTAs to fill the GPU (a few times over
+// where the CTAs are small), none below 4 steps nor, for units of few rows that
+// do not fill it alone, above 32 (1024 tokens: sequences of different lengths
+// then end at about the same time).  Only units that are split have tickets,
+// which lie at a fixed place whatever the call's shape, so that calls of
+// different shapes can share a workspace.
+constexpr int kMinChunk = 4, kMaxChunk = 32;
+constexpr int kShareRows = 64;  // most rows of mma.sync units
 constexpr int kTickets = 2048;
+int step_of(int rows) { return rows == kPrefillRows ? kPrefillStep : kStep; }
 void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, int *chunk) {
-  const int64_t steps = (tokens + kStep - 1) / kStep + 1;  // a range may start inside a step
-  const bool many = units >= (rows > 16 ? 2ll : 8ll) * sms || units > kTickets;
-  const int64_t want = many ? 1 : (4ll * sms + units - 1) / units;
+  const int step = step_of(rows);
+  const int64_t steps = (tokens + step - 1) / step + 1;  // a range may start inside a step
+  const int64_t fill = rows == kPrefillRows ? sms : 4ll * sms;  // CTAs wanted
+  const bool many = units >= (rows <= 16 ? 2 * fill : fill) || units > kTickets;
+  const int64_t want = many ? 1 : (fill + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
   if (c < kMinChunk) c = kMinChunk;
-  if (c > kMaxChunk && !many) c = kMaxChunk;
-  c = (c + kWarps - 1) / kWarps * kWarps;
+  if (c > kMaxChunk && !many && rows <= 16) c = kMaxChunk;
+  c = (c + kMinChunk - 1) / kMinChunk * kMinChunk;
   *chunk = (int)c;
   *splits = (int)((steps + c - 1) / c);
 }
 
 // Query rows (of one head and sequence) per unit: 8 or 16 in a CTA that splits
-// the tokens over its warps, else 64 in one whose warps have 16 each.
-int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 64; }
+// the tokens over its warps, 64 in one whose warps have 16 each, 256 on the
+// 5th-generation tensor cores.
+int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kShareRows ? 64 : kPrefillRows; }
 
 int attn_units(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t heads, int64_t *units,
                int *qtiles) {
@@ -1023,12 +925,12 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   if (rc != HYB_OK) return rc;
   // tokens that one unit sees at most
   const int64_t all = (int64_t)S->max_pages * C->page_size;
+  const int rows = unit_rows((int64_t)S->max_new * (heads / C->kv_heads));
   int64_t tokens = all;
   if (window) {
-    const int64_t span = (int64_t)window + 64 + (int64_t)sinks + 2 * kStep;
+    const int64_t span = (int64_t)window + rows + (int64_t)sinks + 2 * step_of(rows);
     if (span < tokens) tokens = span;
   }
-  const int rows = unit_rows((int64_t)S->max_new * (heads / C->kv_heads));
   int full_splits, full_chunk;
   split_plan(units, rows, all, sms, &full_splits, &full_chunk);
   split_plan(units, rows, tokens, sms, &splits, &chunk);
@@ -1063,6 +965,8 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   if (rc == HYB_OK) rc = encode_pages(C, C->v, &vm);
   if (rc != HYB_OK) return rc;
   cudaStream_t st = (cudaStream_t)stream;
+  if (rows == kPrefillRows)
+    return cache_attention_prefill(p, km, vm, units, C->head_dim, C->type == HYB_I8, st);
   if (C->head_dim == 128)
     return C->type == HYB_I8 ? launch_attention<128, true>(p, km, vm, units, rows, st)
                              : launch_attention<128, false>(p, km, vm, units, rows, st);

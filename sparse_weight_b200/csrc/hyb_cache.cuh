@@ -1,0 +1,116 @@
+// hyb_cache.cuh -- what the kernels of the 8-bit key / value cache share.
+#pragma once
+
+#include "hyb_internal.cuh"
+
+#include <cuda_fp16.h>
+
+namespace hyb {
+
+struct SeqParams {
+  int batch, max_new;
+  int64_t rows;
+  const int32_t *lens, *off, *table;
+  int max_pages;
+  int64_t table_stride;
+  int page_shift;  // log2 of the page size
+};
+
+// Sequence b: its first row, its new tokens and its length; false (flagged)
+// where the caller's arrays contradict one another.
+__device__ __forceinline__ bool sequence(const SeqParams &s, int b, uint32_t *status,
+                                         int64_t &row0, int &fresh, int &len) {
+  len = ld_dep(s.lens + b);
+  bool ok = len >= 0 && (int64_t)len <= ((int64_t)s.max_pages << s.page_shift);
+  if (s.off) {
+    const int64_t o0 = ld_dep(s.off + b), o1 = ld_dep(s.off + b + 1);
+    ok &= o0 >= 0 && o0 <= o1 && o1 <= s.rows && o1 - o0 <= s.max_new;
+    row0 = o0;
+    fresh = (int)(o1 - o0);
+  } else {
+    row0 = (int64_t)b * s.max_new;
+    fresh = s.max_new;
+  }
+  ok &= len == 0 || len >= fresh;
+  if (!ok) atomicOr(status, kStatusBadSeq);
+  return ok;
+}
+
+struct AttnParams {
+  SeqParams s;
+  const uint16_t *Q;
+  int64_t ldq, hsq;
+  uint16_t *O;
+  int64_t ldo, hso;
+  float *lse;
+  int64_t ldl;
+  const float *k_scale, *v_scale;
+  int num_pages, kv_heads, group;
+  float qmul;  // softmax_scale * log2(e)
+  int window, sinks;
+  int qtiles;  // units per sequence and head
+  int splits, chunk;  // CTAs per unit, steps of each
+  float *part;        // [unit][split]: O [16][D], mref [16], l [16]
+  uint32_t *tickets;  // [unit]
+  uint32_t *status;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            int z, int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// two 8-bit values (the low or high half of w) as a pair of fp16, exactly
+template <bool I8, int HALF>
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {
+  uint32_t r;
+  if constexpr (I8) {
+    // 0x6400 | (q + 128) is 1024 + 128 + q in fp16
+    const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, HALF ? 0x4342 : 0x4140);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.0f));
+    r = *reinterpret_cast<const uint32_t *>(&x);
+  } else {
+    const uint16_t two = (uint16_t)(HALF ? w >> 16 : w);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+
+// byte offset of 16-byte chunk c of row r in a box of D-byte rows, as the
+// tensor map's swizzle (128 or 64 bytes) stores it
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if constexpr (D == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+  return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Attention of units of 256 query rows on the tensor cores
+// (hyb_cache_prefill.cu); p.chunk counts steps of 64 tokens there.
+constexpr int kPrefillRows = 256, kPrefillStep = 64;
+int cache_attention_prefill(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm,
+                            int64_t units, int dim, bool i8, cudaStream_t st);
+
+}  // namespace hyb

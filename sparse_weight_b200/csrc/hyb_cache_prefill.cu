@@ -1,0 +1,591 @@
+// Attention over the 8-bit cache for many query rows (prompts, chunks of them),
+// on the 5th-generation tensor cores:
+//
+//   S = Q K^T,  P = exp2(S scaled - max),  O = P V
+//
+// A CTA owns 256 query rows (new token x head of the group) of one sequence and
+// key / value head, as two tiles of 128 (the MMA's M, one tensor-memory lane
+// per row), and walks their visible tokens in steps of 64:
+//
+//   * warp 0 brings the pages' bytes with TMA into a ring of three steps.
+//   * warps 4-7 turn a step's bytes into fp16, once for all 256 rows: K and V as
+//     MMA operands of 64-column halves in the 128-byte swizzle (K by rows of
+//     its contraction, V by rows of tokens, read transposed).
+//   * warp 1 issues S = Q K^T (both tiles, one step ahead) and O += P V with P
+//     from tensor memory.
+//   * warps 8-11 and 12-15, a row per thread, read S, mask it, take the
+//     maximum, and write P as fp16 over S.  O stays in tensor memory; it is
+//     rescaled only where a row's maximum has grown by more than 2^8 since the
+//     last time (P then stays within fp16), which after the first steps hardly
+//     ever happens.
+//
+// Tensor memory: per tile two S buffers of 64 columns and O of D columns.
+// Bound by the exponentials (16 per clock and SM) and the MMAs at about the
+// same rate; converting bytes in the registers of mma.sync fragments instead
+// (hyb_cache.cu) is done again for every 16 rows.
+#include "hyb_cache.cuh"
+#include "hyb_tcgen05.cuh"
+
+namespace hyb {
+namespace {
+
+constexpr int kT = kPrefillStep;
+constexpr int kThreads = 512;
+constexpr int kRaw = 3;  // steps of bytes on their way
+// P is held times 2^7 at the reference maximum, 2^15 at most
+constexpr float kLift = 7.0f, kGrow = 8.0f;
+
+template <int D>
+struct PShape {
+  static constexpr int kQ = 128 * D * 2;                 // a row tile's Q
+  static constexpr int kOp = kT * D * 2;                 // a step's K (or V) in fp16
+  static constexpr int kBytes8 = kT * D;                 // and in 8 bits
+  static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + 4 * kOp;
+  static constexpr int kBytes = kRawOff + kRaw * 2 * kBytes8;
+  static constexpr int kTile = 128 + D;                  // tensor-memory columns of a row tile
+  static constexpr int kTmem = 2 * kTile <= 256 ? 256 : 512;
+  static constexpr int kPart = kPrefillRows * D + 2 * kPrefillRows;
+  static_assert(2 * kTile <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc,
+                                        uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(acc), "r"(idesc)
+      : "memory");
+}
+// A from tensor memory: lane = row, two fp16 of the contraction per column
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc,
+                                        uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(acc), "r"(idesc)
+      : "memory");
+}
+// Operand whose contraction runs along rows (V: rows of tokens), 128-byte
+// swizzle: 64 of the other index per row, the next 64 `half` bytes on (leading
+// byte offset), 8 rows 1024 bytes apart (stride byte offset).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(half >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+#define HYB_R32(r)                                                                             \
+  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),         \
+      "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), \
+      "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),           \
+      "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),           \
+      "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+
+// 32 columns of this thread's lane (tcgen05.wait::ld before the values are used)
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31}, [%32];"
+      : HYB_R32(r)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_got(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // not read before the wait
+}
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+#undef HYB_R32
+
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attention_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
+                                   const __grid_constant__ CUtensorMap vmap) {
+  using Sh = PShape<D>;
+  // D fp32, A and B fp16 (format 0); S: N = 64 tokens; O: N = D, B transposed
+  constexpr uint32_t kM = (uint32_t)(128 >> 4) << 24;
+  constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(kT >> 3) << 17) | kM;
+  constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | kM;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full,
+      s_full[2][2], p_full[2][2], pv_done;
+  __shared__ float s_sc[2][3][4];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
+  __shared__ uint32_t s_tmem, s_last;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = (int)(blockIdx.x % (unsigned)p.splits);
+  const int unit = (int)(blockIdx.x / (unsigned)p.splits);
+  const int qt = unit % p.qtiles;
+  const int h = unit / p.qtiles % p.kv_heads;
+  const int b = unit / p.qtiles / p.kv_heads;
+  int64_t row0;
+  int fresh, len;
+  if (!sequence(p.s, b, p.status, row0, fresh, len)) return;
+  const int G = p.group;
+  const int64_t total = (int64_t)fresh * G;
+  const int64_t u0 = (int64_t)qt * kPrefillRows;
+  if (u0 >= total) return;
+  const int urows = (int)min((int64_t)kPrefillRows, total - u0);
+  const int tiles = urows > 128 ? 2 : 1;
+  const int first = len - fresh;
+
+  // the unit's visible tokens: [0, sinks) and [lo, hi); a query at place q sees t <= q
+  const int i0 = (int)(u0 / G), i1 = (int)((u0 + urows - 1) / G);
+  const int hi = len == 0 ? 0 : first + i1 + 1;
+  const int lo = p.window ? max(0, first + i0 - p.window + 1) : 0;
+  int na = p.window ? (min(p.sinks, hi) + kT - 1) / kT : 0;  // steps of the sinks
+  int nb0 = lo / kT;
+  if (nb0 <= na) na = nb0 = 0;
+  const int nsteps = hi == 0 ? 0 : na + (hi + kT - 1) / kT - nb0;
+  const int active = max(1, (nsteps + p.chunk - 1) / p.chunk);  // CTAs with work
+  if (split >= active) return;
+  const int s_begin = split * p.chunk, n = min(nsteps, s_begin + p.chunk) - s_begin;
+  auto base_of = [&](int j) {
+    const int s = s_begin + j;
+    return (s < na ? s : s - na + nb0) * kT;
+  };
+
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sm = smem_u32(smem);
+  if (tid == 0) {
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&kv_full[s], 4);
+      mbar_init(&kv_empty[s], 1);
+      mbar_init(&s_full[0][s], 1);
+      mbar_init(&s_full[1][s], 1);
+      mbar_init(&p_full[0][s], 128);
+      mbar_init(&p_full[1][s], 128);
+    }
+    mbar_init(&q_full, 128 * tiles);
+    mbar_init(&pv_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&s_tmem)),
+                 "r"(Sh::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int32_t *table = p.s.table + b * p.s.table_stride;
+  // page of a token that exists; page 0 (whose values are masked) otherwise
+  auto page_of = [&](int tok) {
+    int id = 0;
+    if (tok < len) {
+      id = ld_dep(table + (tok >> p.s.page_shift));
+      if (id < 0 || id >= p.num_pages) {
+        atomicOr(p.status, kStatusBadSeq);
+        id = 0;
+      }
+    }
+    return id;
+  };
+
+  bool ok = true;
+  float l = 0.0f, mref = -INFINITY;  // of a softmax thread's row
+  if (warp == 0) {
+    // lane i < 4: tokens 16 i .. of the step
+    const int P = 1 << p.s.page_shift;
+    const int per = min(P, 32);  // tokens of a box
+    int id = n > 0 ? page_of(base_of(0) + 16 * (lane & 3)) : 0;
+    for (int j = 0; j < n; ++j) {
+      const int s = j % kRaw, base = base_of(j);
+      ok = j < kRaw || ring_wait(&raw_empty[s], ((uint32_t)(j / kRaw) & 1u) ^ 1u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], 2 * Sh::kBytes8);
+      __syncwarp();
+      if (lane < 4 && 16 * lane % per == 0) {
+        const int place = (base + 16 * lane) & (P - 1);
+        const uint32_t dst = sm + Sh::kRawOff + s * (2 * Sh::kBytes8) + 16 * lane * D;
+        tma_load_4d(dst, &kmap, 0, place, h, id, &raw_full[s]);
+        tma_load_4d(dst + Sh::kBytes8, &vmap, 0, place, h, id, &raw_full[s]);
+      }
+      if (j + 1 < n) id = page_of(base_of(j + 1) + 16 * (lane & 3));
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      auto scores = [&](int j) {  // S of step j, both tiles
+        ok = ok && ring_wait(&kv_full[j & 1], (uint32_t)(j >> 1) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        for (int r = 0; r < tiles; ++r) {
+          const uint32_t q = sm + Sh::kQOff + r * Sh::kQ, k = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(tmem + r * Sh::kTile + (j & 1) * kT,
+                    sw128_desc(q + (kk >> 2) * (128 * 128) + (kk & 3) * 32),
+                    sw128_desc(k + (kk >> 2) * (kT * 128) + (kk & 3) * 32), kk != 0, kIdS);
+          umma_commit(&s_full[r][j & 1]);
+        }
+      };
+      ok = ring_wait(&q_full, 0u);
+      scores(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) {
+          // the other S buffer holds P of the step before: its product has to be done
+          if (j > 0) ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
+          scores(j + 1);
+        }
+        for (int r = 0; r < tiles && ok; ++r) {
+          ok = ring_wait(&p_full[r][j & 1], (uint32_t)(j >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp + Sh::kOp;
+#pragma unroll
+          for (int kk = 0; kk < kT / 16; ++kk)
+            umma_ts(tmem + r * Sh::kTile + 128, tmem + r * Sh::kTile + (j & 1) * kT + 8 * kk,
+                    sw128_desc_mn(v + kk * 2048, kT * 128), (j | kk) != 0, kIdO);
+        }
+        if (!ok) break;
+        umma_commit(&kv_empty[j & 1]);
+        umma_commit(&pv_done);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    // bytes to fp16.  A thread takes 16-byte chunk c of token tok; tokens that no
+    // row sees become zeros, whatever lies there.
+    const int e = tid - 128;
+    constexpr int kItems = kT * (D / 16) / 128;
+    int tok[kItems], ch[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      if (D == 128) {
+        // 8 neighbours: 4 chunks of a token and the other 4 of the next one, so
+        // that neither the reads nor the writes meet in a bank
+        tok[i] = (e >> 2) + 32 * (i >> 1);
+        ch[i] = (e & 3) + 4 * (((e >> 2) ^ i) & 1);
+      } else {
+        tok[i] = (e >> 2) + 32 * i;
+        ch[i] = e & 3;
+      }
+    }
+    // scales of the step's groups of 16 tokens: lane i < 4 of warp 4, the pages
+    // two steps and the scales one step ahead
+    auto scales = [&](int id, float &ks, float &vs) {
+      ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
+      vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
+    };
+    const bool sc = warp == 4 && lane < 4;
+    float ks = 0.0f, vs = 1.0f;
+    int id = 0;
+    if (sc && n > 0) {
+      scales(page_of(base_of(0) + 16 * lane), ks, vs);
+      if (n > 1) id = page_of(base_of(1) + 16 * lane);
+    }
+    for (int j = 0; j < n; ++j) {
+      const int s = j % kRaw, base = base_of(j);
+      ok = ring_wait(&raw_full[s], (uint32_t)(j / kRaw) & 1u) &&
+           (j < 2 || ring_wait(&kv_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u));
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      if (sc) {
+        s_sc[j & 1][0][lane] = ks;
+        s_sc[j & 1][1][lane] = __log2f(vs);
+        s_sc[j & 1][2][lane] = __fdividef(1.0f, vs);
+        if (j + 1 < n) scales(id, ks, vs);
+        if (j + 2 < n) id = page_of(base_of(j + 2) + 16 * lane);
+      }
+      const bool whole = base + kT <= hi && (base >= lo || base + kT <= p.sinks);
+      const uint32_t raw = sm + Sh::kRawOff + s * (2 * Sh::kBytes8);
+      const uint32_t op = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        uint4 x[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) x[i] = lds16(raw + kv * Sh::kBytes8 + swz<D>(tok[i], ch[i]));
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          if (!whole) {
+            const int at = base + tok[i];
+            if (!(at < hi && (at >= lo || at < p.sinks))) x[i] = make_uint4(0, 0, 0, 0);
+          }
+          // fp16 chunks 2 c, 2 c + 1 of the row: half c / 4
+          const uint32_t row = op + kv * Sh::kOp + (ch[i] >> 2) * (kT * 128) + tok[i] * 128;
+          const int c = (2 * ch[i]) & 7, r7 = tok[i] & 7;
+          sts16(row + ((c ^ r7) << 4), to_f16x2<I8, 0>(x[i].x), to_f16x2<I8, 1>(x[i].x),
+                to_f16x2<I8, 0>(x[i].y), to_f16x2<I8, 1>(x[i].y));
+          sts16(row + (((c + 1) ^ r7) << 4), to_f16x2<I8, 0>(x[i].z), to_f16x2<I8, 1>(x[i].z),
+                to_f16x2<I8, 0>(x[i].w), to_f16x2<I8, 1>(x[i].w));
+        }
+      }
+      // generic-proxy writes, read next by tcgen05.mma (async proxy)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&kv_full[j & 1]);
+        mbar_arrive(&raw_empty[s]);
+      }
+    }
+  } else if (warp >= 8 && ((warp - 8) >> 2) < tiles) {
+    // softmax: a row per thread
+    const int r = (warp - 8) >> 2;
+    const int trow = 32 * (warp & 3) + lane;       // row of the tile, tensor-memory lane
+    const int row = 128 * r + trow;                // row of the unit
+    const bool live = row < urows;
+    const int64_t rr = u0 + (live ? row : 0);
+    const int i = (int)(rr / G), hd = h * G + (int)(rr % G);
+    const int bhi = live && len > 0 ? first + i + 1 : 0;
+    const int blo = p.window ? first + i - p.window + 1 : 0;
+    // Q's row times a power of two that brings its largest value to [128, 256)
+    float qm;
+    {
+      const uint16_t *src = p.Q + (row0 + i) * p.ldq + hd * p.hsq;
+      uint4 w[D / 8];
+      uint32_t a = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        w[c] = ld_dep16(src + 8 * c);
+        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a = max(a, max((x[e] & 0x7FFFu) >> 7, (x[e] >> 23) & 0xFFu));
+      }
+      a = max(a, 8u);
+      const float f = __uint_as_float((261u - a) << 23);
+      qm = p.qmul * __uint_as_float((a - 7u) << 23);  // 2^(a - 134)
+      const uint32_t q = sm + Sh::kQOff + r * Sh::kQ + trow * 128;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 v = live ? __floats2half2_rn(bf16_lo(x[e]) * f, bf16_hi(x[e]) * f)
+                                 : __float2half2_rn(0.0f);
+          y[e] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        sts16(q + (c >> 3) * (128 * 128) + (((c & 7) ^ (trow & 7)) << 4), y[0], y[1], y[2], y[3]);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(&q_full);
+    }
+    const uint32_t tl = tmem + r * Sh::kTile + ((uint32_t)(32 * (warp & 3)) << 16);
+    // the warp's narrowest and widest bounds: outside them a step needs no mask
+    const int whi = __reduce_min_sync(0xFFFFFFFFu, live ? bhi : INT32_MAX);
+    const int wlo = __reduce_max_sync(0xFFFFFFFFu, live ? blo : 0);
+    for (int j = 0; j < n; ++j) {
+      const int base = base_of(j);
+      ok = ring_wait(&s_full[r][j & 1], (uint32_t)(j >> 1) & 1u) &&
+           ring_wait(&kv_full[j & 1], (uint32_t)(j >> 1) & 1u);  // (s_sc of the step)
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[kT];
+      tmem_get(tl + (j & 1) * kT, x);
+      tmem_get(tl + (j & 1) * kT + 32, x + 32);
+      tmem_got(x);
+      tmem_got(x + 32);
+      const bool edge = base + kT > whi || base < wlo;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float f = s_sc[j & 1][0][c] * qm, lv = s_sc[j & 1][1][c];
+#pragma unroll
+        for (int e = 16 * c; e < 16 * c + 16; ++e) {
+          float v = fmaf(__uint_as_float(x[e]), f, lv);
+          if (edge) {
+            const int at = base + e;
+            if (!(at < bhi && (at >= blo || at < p.sinks))) v = -INFINITY;
+          }
+          mx = fmaxf(mx, v);
+          x[e] = __float_as_uint(v);
+        }
+      }
+      const bool fresh_row = mref == -INFINITY;  // nothing of this row in O yet
+      const bool need = mx > (fresh_row ? -INFINITY : mref + kGrow);
+      const bool rescale = need && !fresh_row;
+      if (__any_sync(0xFFFFFFFFu, rescale)) {
+        const float corr = rescale ? ex2(mref - mx) : 1.0f;
+        l *= corr;
+        ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t y[32];
+          tmem_get(tl + 128 + 32 * c, y);
+          tmem_got(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+          tmem_put(tl + 128 + 32 * c, y);
+        }
+      }
+      if (need) mref = mx;
+      const float ref = (mref == -INFINITY ? 0.0f : mref) - kLift;
+      uint32_t pk[kT / 2];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 16 * c; e < 16 * c + 16; e += 2) {
+          const float a = ex2(__uint_as_float(x[e]) - ref), d = ex2(__uint_as_float(x[e + 1]) - ref);
+          sum += a + d;
+          const __half2 hp = __floats2half2_rn(a, d);
+          pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hp);
+        }
+        l = fmaf(sum, s_sc[j & 1][2][c], l);
+      }
+      tmem_put(tl + (j & 1) * kT, pk);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      // (one barrier per buffer: a fast warp may be a step ahead of a slow one)
+      mbar_arrive(&p_full[r][j & 1]);
+    }
+    // O: the last step's product is done
+    if (n > 0 && ok) {
+      ok = ring_wait(&pv_done, (uint32_t)(n - 1) & 1u);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    tc_fence_after();
+    const bool alone = active == 1;
+    float *mypart = alone ? nullptr : p.part + ((int64_t)unit * p.splits + split) * Sh::kPart;
+    const bool some = l != 0.0f;  // NaN counts
+    const float inv = some ? 1.0f / l : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t y[32];
+      if (n > 0 && ok) {
+        tmem_get(tl + 128 + 32 * c, y);
+        tmem_got(y);
+      }
+      if (!live) continue;
+      // a row without a visible token: its products may be of anything
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!some) y[e] = 0;
+      if (alone) {
+        uint16_t *to = p.O + (row0 + i) * p.ldo + hd * p.hso + 32 * c;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t o[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            o[q] = f32_to_bf16_rne(__uint_as_float(y[e + 2 * q]) * inv) |
+                   ((uint32_t)f32_to_bf16_rne(__uint_as_float(y[e + 2 * q + 1]) * inv) << 16);
+          *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<uint4 *>(mypart + row * D + 32 * c + e) =
+              make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+      }
+    }
+    if (live) {
+      if (!alone) {
+        mypart[kPrefillRows * D + row] = mref;
+        mypart[kPrefillRows * D + kPrefillRows + row] = l;
+      } else if (p.lse) {
+        p.lse[(row0 + i) * p.ldl + hd] =
+            some ? (mref - kLift + log2f(l)) * 0.693147180559945309f : -INFINITY;
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicOr(p.status, kStatusTimeout);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(Sh::kTmem)
+                 : "memory");
+  }
+  if (active == 1) return;
+
+  // the unit's last CTA adds the parts in order
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t at = atomicAdd(p.tickets + unit, 1u);
+    s_last = at == (uint32_t)active - 1u;
+    if (s_last) p.tickets[unit] = 0;  // ready for the next call
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  const float *up = p.part + (int64_t)unit * p.splits * Sh::kPart;
+  for (int e = tid; e < urows * (D / 4); e += kThreads) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    float mx = -INFINITY;
+    for (int s = 0; s < active; ++s)
+      mx = fmaxf(mx, __ldcg(up + (int64_t)s * Sh::kPart + kPrefillRows * D + row));
+    const float safe = mx == -INFINITY ? 0.0f : mx;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float den = 0.0f;
+    for (int s = 0; s < active; ++s) {
+      const float *q = up + (int64_t)s * Sh::kPart;
+      const float f = ex2(__ldcg(q + kPrefillRows * D + row) - safe);
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(q + row * D + d));
+      num.x = fmaf(f, x.x, num.x);
+      num.y = fmaf(f, x.y, num.y);
+      num.z = fmaf(f, x.z, num.z);
+      num.w = fmaf(f, x.w, num.w);
+      den = fmaf(f, __ldcg(q + kPrefillRows * D + kPrefillRows + row), den);
+    }
+    const int64_t rr = u0 + row;
+    const int i = (int)(rr / G), hd = h * G + (int)(rr % G);
+    const float inv = den != 0.0f ? 1.0f / den : 0.0f;
+    *reinterpret_cast<uint2 *>(p.O + (row0 + i) * p.ldo + hd * p.hso + d) =
+        make_uint2(f32_to_bf16_rne(num.x * inv) | ((uint32_t)f32_to_bf16_rne(num.y * inv) << 16),
+                   f32_to_bf16_rne(num.z * inv) | ((uint32_t)f32_to_bf16_rne(num.w * inv) << 16));
+    if (d == 0 && p.lse)
+      p.lse[(row0 + i) * p.ldl + hd] =
+          den != 0.0f ? (mx - kLift + log2f(den)) * 0.693147180559945309f : -INFINITY;
+  }
+}
+
+template <int D, bool I8>
+int launch(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int64_t units,
+           cudaStream_t st) {
+  const int dyn = PShape<D>::kBytes + 1024;
+  if (cudaFuncSetAttribute(cache_attention_prefill_kernel<D, I8>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+    return HYB_ERR_CUDA;
+  if (units * p.splits > INT32_MAX) return HYB_ERR_UNSUPPORTED;
+  return launch_dependent(cache_attention_prefill_kernel<D, I8>,
+                          dim3((unsigned)(units * p.splits)), kThreads, dyn, 1, st, p, km, vm);
+}
+
+}  // namespace
+
+int cache_attention_prefill(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm,
+                            int64_t units, int dim, bool i8, cudaStream_t st) {
+  if (dim == 128)
+    return i8 ? launch<128, true>(p, km, vm, units, st) : launch<128, false>(p, km, vm, units, st);
+  return i8 ? launch<64, true>(p, km, vm, units, st) : launch<64, false>(p, km, vm, units, st);
+}
+
+}  // namespace hyb

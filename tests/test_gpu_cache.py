@@ -100,6 +100,10 @@ ATT = [
     ([90, 33], [33, 33], 3, 1, 128, 64, "e4m3"),
     ([200, 64, 1], [200, 17, 0], 16, 2, 128, 32, "e4m3"),
     ([257], [130], 40, 8, 64, 64, "i8"),
+    ([700, 300], [70, 70], 4, 1, 128, 16, "i8"),
+    ([600, 0, 90, 64], [100, 40, 90, 1], 6, 2, 64, 16, "e4m3"),
+    ([1500], [20], 8, 1, 128, 32, "e4m3"),
+    ([129, 65], [129, 65], 2, 1, 128, 64, "e4m3"),
 ]
 
 
@@ -121,7 +125,7 @@ def test_attention(i, order):
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (31, 0), (33, 40), (100, 20), (5000, 3), (64, 5000)])
-@pytest.mark.parametrize("i", [2, 3, 5, 7, 8, 10, 11])
+@pytest.mark.parametrize("i", [2, 3, 5, 7, 8, 10, 11, 12, 13, 14])
 def test_attention_window(i, window, sinks):
     lens, new, heads, kvh, dim, size, type_ = ATT[i]
     C, table, off = setup(lens, new, kvh, dim, size, type_, seed=i)
