@@ -32,6 +32,7 @@ namespace {
 constexpr int kT = kPrefillStep;
 constexpr int kThreads = 512;
 constexpr int kRaw = 3;  // steps of bytes on their way
+constexpr int kKv = 3;   // steps of fp16 operands
 // P is held times 2^7 at the reference maximum, 2^15 at most
 constexpr float kLift = 7.0f, kGrow = 8.0f;
 
@@ -40,7 +41,7 @@ struct PShape {
   static constexpr int kQ = 128 * D * 2;                 // a row tile's Q
   static constexpr int kOp = kT * D * 2;                 // a step's K (or V) in fp16
   static constexpr int kBytes8 = kT * D;                 // and in 8 bits
-  static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + 4 * kOp;
+  static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + 2 * kKv * kOp;
   static constexpr int kBytes = kRawOff + kRaw * 2 * kBytes8;
   static constexpr int kTile = 128 + D;                  // tensor-memory columns of a row tile
   static constexpr int kTmem = 2 * kTile <= 256 ? 256 : 512;
@@ -114,6 +115,28 @@ __device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
 }
 #undef HYB_R32
 
+// on pairs of fp32: (a, b) = (a, b) * f + o, and sum += (a, b)
+__device__ __forceinline__ uint64_t pair(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint32_t &a, uint32_t &b, uint64_t f, uint64_t o) {
+  asm("{\n\t.reg .b64 t;\n\t"
+      "mov.b64 t, {%0, %1};\n\t"
+      "fma.rn.f32x2 t, t, %2, %3;\n\t"
+      "mov.b64 {%0, %1}, t;\n\t}"
+      : "+r"(a), "+r"(b)
+      : "l"(f), "l"(o));
+}
+__device__ __forceinline__ void add2(uint64_t &sum, float a, float b) {
+  asm("{\n\t.reg .b64 t;\n\t"
+      "mov.b64 t, {%1, %2};\n\t"
+      "add.rn.f32x2 %0, %0, t;\n\t}"
+      : "+l"(sum)
+      : "f"(a), "f"(b));
+}
+
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -129,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(kT >> 3) << 17) | kM;
   constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | kM;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[2], kv_empty[2], q_full,
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kKv], kv_empty[kKv], q_full,
       s_full[2][2], p_full[2][2], pv_done;
-  __shared__ float s_sc[2][3][4];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
+  __shared__ float s_sc[kKv][3][4];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
   __shared__ uint32_t s_tmem, s_last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -175,9 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKv; ++s) {
       mbar_init(&kv_full[s], 4);
       mbar_init(&kv_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[0][s], 1);
       mbar_init(&s_full[1][s], 1);
       mbar_init(&p_full[0][s], 128);
@@ -213,7 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   bool ok = true;
-  float l = 0.0f, mref = -INFINITY;  // of a softmax thread's row
+  // of a softmax thread's row: the sum of P / vs, the reference (P = exp2(t - ref)),
+  // and whether nothing of it lies in O yet
+  float l = 0.0f, ref = 0.0f;
+  bool fresh_row = true;
   if (warp == 0) {
     // lane i < 4: tokens 16 i .. of the step
     const int P = 1 << p.s.page_shift;
@@ -237,11 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && n > 0) {
       auto scores = [&](int j) {  // S of step j, both tiles
-        ok = ok && ring_wait(&kv_full[j & 1], (uint32_t)(j >> 1) & 1u);
+        ok = ok && ring_wait(&kv_full[j % kKv], (uint32_t)(j / kKv) & 1u);
         if (!ok) return;
         tc_fence_after();
         for (int r = 0; r < tiles; ++r) {
-          const uint32_t q = sm + Sh::kQOff + r * Sh::kQ, k = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp;
+          const uint32_t q = sm + Sh::kQOff + r * Sh::kQ, k = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             umma_ss(tmem + r * Sh::kTile + (j & 1) * kT,
@@ -262,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = ring_wait(&p_full[r][j & 1], (uint32_t)(j >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp + Sh::kOp;
+          const uint32_t v = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp + Sh::kOp;
 #pragma unroll
           for (int kk = 0; kk < kT / 16; ++kk)
             umma_ts(tmem + r * Sh::kTile + 128, tmem + r * Sh::kTile + (j & 1) * kT + 8 * kk,
                     sw128_desc_mn(v + kk * 2048, kT * 128), (j | kk) != 0, kIdO);
         }
         if (!ok) break;
-        umma_commit(&kv_empty[j & 1]);
+        umma_commit(&kv_empty[j % kKv]);
         umma_commit(&pv_done);
       }
     }
@@ -308,19 +336,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < n; ++j) {
       const int s = j % kRaw, base = base_of(j);
       ok = ring_wait(&raw_full[s], (uint32_t)(j / kRaw) & 1u) &&
-           (j < 2 || ring_wait(&kv_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u));
+           (j < kKv || ring_wait(&kv_empty[j % kKv], ((uint32_t)(j / kKv) & 1u) ^ 1u));
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       if (sc) {
-        s_sc[j & 1][0][lane] = ks;
-        s_sc[j & 1][1][lane] = __log2f(vs);
-        s_sc[j & 1][2][lane] = __fdividef(1.0f, vs);
+        s_sc[j % kKv][0][lane] = ks;
+        s_sc[j % kKv][1][lane] = __log2f(vs);
+        s_sc[j % kKv][2][lane] = __fdividef(1.0f, vs);
         if (j + 1 < n) scales(id, ks, vs);
         if (j + 2 < n) id = page_of(base_of(j + 2) + 16 * lane);
       }
       const bool whole = base + kT <= hi && (base >= lo || base + kT <= p.sinks);
       const uint32_t raw = sm + Sh::kRawOff + s * (2 * Sh::kBytes8);
-      const uint32_t op = sm + Sh::kOpOff + (j & 1) * 2 * Sh::kOp;
+      const uint32_t op = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         uint4 x[kItems];
@@ -345,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&kv_full[j & 1]);
+        mbar_arrive(&kv_full[j % kKv]);
         mbar_arrive(&raw_empty[s]);
       }
     }
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < n; ++j) {
       const int base = base_of(j);
       ok = ring_wait(&s_full[r][j & 1], (uint32_t)(j >> 1) & 1u) &&
-           ring_wait(&kv_full[j & 1], (uint32_t)(j >> 1) & 1u);  // (s_sc of the step)
+           ring_wait(&kv_full[j % kKv], (uint32_t)(j / kKv) & 1u);  // (s_sc of the step)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -407,56 +435,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_get(tl + (j & 1) * kT + 32, x + 32);
       tmem_got(x);
       tmem_got(x + 32);
-      const bool edge = base + kT > whi || base < wlo;
-      float mx = -INFINITY;
+      // exponents against the reference: s * scale + log2(vs) - ref
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float f = s_sc[j & 1][0][c] * qm, lv = s_sc[j & 1][1][c];
+        const uint64_t f = pair(s_sc[j % kKv][0][c] * qm), o = pair(s_sc[j % kKv][1][c] - ref);
 #pragma unroll
-        for (int e = 16 * c; e < 16 * c + 16; ++e) {
-          float v = fmaf(__uint_as_float(x[e]), f, lv);
-          if (edge) {
-            const int at = base + e;
-            if (!(at < bhi && (at >= blo || at < p.sinks))) v = -INFINITY;
-          }
-          mx = fmaxf(mx, v);
-          x[e] = __float_as_uint(v);
+        for (int e = 16 * c; e < 16 * c + 16; e += 2) fma2(x[e], x[e + 1], f, o);
+      }
+      if (base + kT > whi || base < wlo) {  // some row of the warp does not see it whole
+#pragma unroll
+        for (int e = 0; e < kT; ++e) {
+          const int at = base + e;
+          if (!(at < bhi && (at >= blo || at < p.sinks))) x[e] = 0xFF800000u;  // -infinity
         }
       }
-      const bool fresh_row = mref == -INFINITY;  // nothing of this row in O yet
-      const bool need = mx > (fresh_row ? -INFINITY : mref + kGrow);
-      const bool rescale = need && !fresh_row;
-      if (__any_sync(0xFFFFFFFFu, rescale)) {
-        const float corr = rescale ? ex2(mref - mx) : 1.0f;
-        l *= corr;
-        ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
+      float mx = __uint_as_float(x[0]);
+#pragma unroll
+      for (int e = 1; e < kT; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+      const bool need = mx > (fresh_row ? -INFINITY : kLift + kGrow);
+      if (__any_sync(0xFFFFFFFFu, need)) {
+        // a new reference: what lies in O and l counts against the old one
+        const float by = need ? mx - kLift : 0.0f;
+        const bool rescale = need && !fresh_row;
+        ref += by;
+#pragma unroll
+        for (int e = 0; e < kT; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - by);
+        if (__any_sync(0xFFFFFFFFu, rescale)) {
+          const float corr = rescale ? ex2(-by) : 1.0f;
+          l *= corr;
+          ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t y[32];
-          tmem_get(tl + 128 + 32 * c, y);
-          tmem_got(y);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t y[32];
+            tmem_get(tl + 128 + 32 * c, y);
+            tmem_got(y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
-          tmem_put(tl + 128 + 32 * c, y);
+            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+            tmem_put(tl + 128 + 32 * c, y);
+          }
         }
+        fresh_row = fresh_row && !need;
       }
-      if (need) mref = mx;
-      const float ref = (mref == -INFINITY ? 0.0f : mref) - kLift;
       uint32_t pk[kT / 2];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        float sum = 0.0f;
+        uint64_t sum = 0;  // a pair of sums
 #pragma unroll
         for (int e = 16 * c; e < 16 * c + 16; e += 2) {
-          const float a = ex2(__uint_as_float(x[e]) - ref), d = ex2(__uint_as_float(x[e + 1]) - ref);
-          sum += a + d;
+          const float a = ex2(__uint_as_float(x[e])), d = ex2(__uint_as_float(x[e + 1]));
+          add2(sum, a, d);
           const __half2 hp = __floats2half2_rn(a, d);
           pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hp);
         }
-        l = fmaf(sum, s_sc[j & 1][2][c], l);
+        const float lo2 = __uint_as_float((uint32_t)sum), hi2 = __uint_as_float((uint32_t)(sum >> 32));
+        l = fmaf(lo2 + hi2, s_sc[j % kKv][2][c], l);
       }
       tmem_put(tl + (j & 1) * kT, pk);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -506,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (live) {
       if (!alone) {
-        mypart[kPrefillRows * D + row] = mref;
+        mypart[kPrefillRows * D + row] = fresh_row ? -INFINITY : ref;
         mypart[kPrefillRows * D + kPrefillRows + row] = l;
       } else if (p.lse) {
         p.lse[(row0 + i) * p.ldl + hd] =
-            some ? (mref - kLift + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            some ? (ref + log2f(l)) * 0.693147180559945309f : -INFINITY;
       }
     }
   }
@@ -563,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    f32_to_bf16_rne(num.z * inv) | ((uint32_t)f32_to_bf16_rne(num.w * inv) << 16));
     if (d == 0 && p.lse)
       p.lse[(row0 + i) * p.ldl + hd] =
-          den != 0.0f ? (mx - kLift + log2f(den)) * 0.693147180559945309f : -INFINITY;
+          den != 0.0f ? (mx + log2f(den)) * 0.693147180559945309f : -INFINITY;
   }
 }
 

@@ -53,8 +53,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 // microsecond per ring slot.  Gives up (returns false) after about 2^31 SM
 // clocks, so a phase that never completes ends the CTA's pipeline.
 __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
-  const long long t0 = clock64();
-  do {
+  long long t0 = 0;
+  for (;;) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -64,8 +64,10 @@ __device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity), "r"(200000u)  // hint: 200 us
         : "memory");
     if (ok) return true;
-  } while (clock64() - t0 < (1ll << 31));
-  return false;
+    const long long now = clock64();
+    if (t0 == 0) t0 = now;  // (the clock is read only where the first try did not do)
+    if (now - t0 >= (1ll << 31)) return false;
+  }
 }
 
 }  // namespace hyb
