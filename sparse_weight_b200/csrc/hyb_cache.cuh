@@ -108,8 +108,8 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 }
 
 // Attention of units of 256 query rows on the tensor cores
-// (hyb_cache_prefill.cu); p.chunk counts steps of 64 tokens there.
-constexpr int kPrefillRows = 256, kPrefillStep = 64;
+// (hyb_cache_prefill.cu); p.chunk counts steps of 128 tokens there.
+constexpr int kPrefillRows = 256, kPrefillStep = 128;
 int cache_attention_prefill(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm,
                             int64_t units, int dim, bool i8, cudaStream_t st);
 

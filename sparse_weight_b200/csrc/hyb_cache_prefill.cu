@@ -5,24 +5,23 @@
 //
 // A CTA owns 256 query rows (new token x head of the group) of one sequence and
 // key / value head, as two tiles of 128 (the MMA's M, one tensor-memory lane
-// per row), and walks their visible tokens in steps of 64:
+// per row), and walks their visible tokens in steps of 128:
 //
-//   * warp 0 brings the pages' bytes with TMA into a ring of three steps.
-//   * warps 4-7 turn a step's bytes into fp16, once for all 256 rows: K and V as
-//     MMA operands of 64-column halves in the 128-byte swizzle (K by rows of
-//     its contraction, V by rows of tokens, read transposed).
-//   * warp 1 issues S = Q K^T (both tiles, one step ahead) and O += P V with P
-//     from tensor memory.
+//   * warp 0 brings the pages' bytes with TMA, a step's keys and values in turn.
+//   * warps 4-7 turn them into fp16, once for all 256 rows: MMA operands of
+//     64-column halves in the 128-byte swizzle (K by rows of its contraction,
+//     V by rows of tokens, read transposed), in a ring of four.
+//   * warp 1 issues S = Q K^T and O += P V with P from tensor memory, for one
+//     tile while the other one's softmax is computed.
 //   * warps 8-11 and 12-15, a row per thread, read S, mask it, take the
 //     maximum, and write P as fp16 over S.  O stays in tensor memory; it is
-//     rescaled only where a row's maximum has grown by more than 2^8 since the
-//     last time (P then stays within fp16), which after the first steps hardly
-//     ever happens.
+//     rescaled only where a row's maximum has grown by more than 2^11 since the
+//     last time (P then stays within fp16).
 //
-// Tensor memory: per tile two S buffers of 64 columns and O of D columns.
-// Bound by the exponentials (16 per clock and SM) and the MMAs at about the
-// same rate; converting bytes in the registers of mma.sync fragments instead
-// (hyb_cache.cu) is done again for every 16 rows.
+// Tensor memory: per tile 128 columns of S and D of O.  Bound by the
+// exponentials (16 per clock and SM: 2048 clocks for 256 x 128) and the MMAs at
+// about the same rate.  With steps of 64 tokens the MMAs of N = 64 took longer
+// than the exponentials: they read the 128 rows of Q for half the products.
 #include "hyb_cache.cuh"
 #include "hyb_tcgen05.cuh"
 
@@ -31,41 +30,48 @@ namespace {
 
 constexpr int kT = kPrefillStep;
 constexpr int kThreads = 512;
-constexpr int kRaw = 3;  // steps of bytes on their way
-constexpr int kKv = 3;   // steps of fp16 operands
-// P is held times 2^7 at the reference maximum, 2^15 at most
-constexpr float kLift = 7.0f, kGrow = 8.0f;
+constexpr int kRaw = 2;  // keys or values of a step on their way
+constexpr int kOps = 4;  // and as fp16 operands
+constexpr int kSc = 3;   // steps whose scales are held
+// P is held times 2^4 at the reference, 2^15 at most: fp16's smallest step is then
+// 2^-28 of the largest P
+constexpr float kLift = 4.0f, kGrow = 11.0f;
 
 template <int D>
 struct PShape {
-  static constexpr int kQ = 128 * D * 2;                 // a row tile's Q
-  static constexpr int kOp = kT * D * 2;                 // a step's K (or V) in fp16
-  static constexpr int kBytes8 = kT * D;                 // and in 8 bits
-  static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + 2 * kKv * kOp;
-  static constexpr int kBytes = kRawOff + kRaw * 2 * kBytes8;
-  static constexpr int kTile = 128 + D;                  // tensor-memory columns of a row tile
-  static constexpr int kTmem = 2 * kTile <= 256 ? 256 : 512;
+  static constexpr int kQ = 128 * D * 2;    // a row tile's Q
+  static constexpr int kOp = kT * D * 2;    // a step's K (or V) in fp16
+  static constexpr int kBytes8 = kT * D;    // and in 8 bits
+  static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + kOps * kOp;
+  static constexpr int kBytes = kRawOff + kRaw * kBytes8;
+  static constexpr int kTile = kT + D;      // tensor-memory columns of a row tile
   static constexpr int kPart = kPrefillRows * D + 2 * kPrefillRows;
   static_assert(2 * kTile <= 512, "tensor memory");
 };
+constexpr int kTmem = 512;
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc,
-                                        uint32_t idesc) {
+// The MMA warp runs as a whole and only its leader's instructions take effect:
+// operands then stay in uniform registers (from a branch of one lane they were
+// moved there one by one, which took longer than the products).
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                        uint32_t acc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(acc), "r"(idesc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(acc), "r"(idesc), "r"(leader)
       : "memory");
 }
 // A from tensor memory: lane = row, two fp16 of the contraction per column
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc,
-                                        uint32_t idesc) {
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
+                                        uint32_t acc, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(acc), "r"(idesc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(acc), "r"(idesc), "r"(leader)
       : "memory");
 }
 // Operand whose contraction runs along rows (V: rows of tokens), 128-byte
@@ -88,7 +94,7 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half)
       "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
 
 // 32 columns of this thread's lane (tcgen05.wait::ld before the values are used)
-__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t *r) {
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
@@ -96,12 +102,13 @@ __device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t *r) {
       : HYB_R32(r)
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_got(uint32_t *r) {
+template <int N>
+__device__ __forceinline__ void tmem_got(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // not read before the wait
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));  // not read before the wait
 }
-__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
@@ -114,6 +121,15 @@ __device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t *r) {
       : "memory");
 }
 #undef HYB_R32
+
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 
 // on pairs of fp32: (a, b) = (a, b) * f + o, and sum += (a, b)
 __device__ __forceinline__ uint64_t pair(float v) {
@@ -147,14 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attention_prefill_kernel(const AttnParams p, const __grid_constant__ CUtensorMap kmap,
                                    const __grid_constant__ CUtensorMap vmap) {
   using Sh = PShape<D>;
-  // D fp32, A and B fp16 (format 0); S: N = 64 tokens; O: N = D, B transposed
+  // D fp32, A and B fp16 (format 0); S: N = 128 tokens; O: N = D, B transposed
   constexpr uint32_t kM = (uint32_t)(128 >> 4) << 24;
   constexpr uint32_t kIdS = (1u << 4) | ((uint32_t)(kT >> 3) << 17) | kM;
   constexpr uint32_t kIdO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | kM;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], kv_full[kKv], kv_empty[kKv], q_full,
-      s_full[2][2], p_full[2][2], pv_done;
-  __shared__ float s_sc[kKv][3][4];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
+  __shared__ __align__(8) uint64_t raw_full[kRaw], raw_empty[kRaw], op_full[kOps], op_empty[kOps],
+      sc_full[kSc], q_full, s_full[2], p_full[2], pv_done[2], o_full[2];
+  __shared__ float s_sc[kSc][3][kT / 16];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
   __shared__ uint32_t s_tmem, s_last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -198,24 +214,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
-    for (int s = 0; s < kKv; ++s) {
-      mbar_init(&kv_full[s], 4);
-      mbar_init(&kv_empty[s], 1);
+    for (int s = 0; s < kOps; ++s) {
+      mbar_init(&op_full[s], 4);
+      mbar_init(&op_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[0][s], 1);
-      mbar_init(&s_full[1][s], 1);
-      mbar_init(&p_full[0][s], 128);
-      mbar_init(&p_full[1][s], 128);
+    for (int s = 0; s < kSc; ++s) mbar_init(&sc_full[s], 1);
+    for (int r = 0; r < 2; ++r) {
+      mbar_init(&s_full[r], 1);
+      mbar_init(&p_full[r], 128);
+      mbar_init(&pv_done[r], 1);
+      mbar_init(&o_full[r], 1);
     }
     mbar_init(&q_full, 128 * tiles);
-    mbar_init(&pv_done, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&s_tmem)),
-                 "r"(Sh::kTmem)
+                 "r"(kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -243,125 +259,135 @@ __global__ void __launch_bounds__(kThreads, 1)
   float l = 0.0f, ref = 0.0f;
   bool fresh_row = true;
   if (warp == 0) {
-    // lane i < 4: tokens 16 i .. of the step
+    // lane i < 8: tokens 16 i .. of the step
     const int P = 1 << p.s.page_shift;
     const int per = min(P, 32);  // tokens of a box
-    int id = n > 0 ? page_of(base_of(0) + 16 * (lane & 3)) : 0;
-    for (int j = 0; j < n; ++j) {
-      const int s = j % kRaw, base = base_of(j);
-      ok = j < kRaw || ring_wait(&raw_empty[s], ((uint32_t)(j / kRaw) & 1u) ^ 1u);
+    const int mine = 16 * (lane & 7);
+    int id = n > 0 ? page_of(base_of(0) + mine) : 0, next = 0;
+    for (int h2 = 0; h2 < 2 * n; ++h2) {  // keys, then values of each step
+      const int s = h2 % kRaw, j = h2 >> 1;
+      if (!(h2 & 1) && j + 1 < n) next = page_of(base_of(j + 1) + mine);
+      ok = h2 < kRaw || ring_wait(&raw_empty[s], ((uint32_t)(h2 / kRaw) & 1u) ^ 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], 2 * Sh::kBytes8);
+      if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], Sh::kBytes8);
       __syncwarp();
-      if (lane < 4 && 16 * lane % per == 0) {
-        const int place = (base + 16 * lane) & (P - 1);
-        const uint32_t dst = sm + Sh::kRawOff + s * (2 * Sh::kBytes8) + 16 * lane * D;
-        tma_load_4d(dst, &kmap, 0, place, h, id, &raw_full[s]);
-        tma_load_4d(dst + Sh::kBytes8, &vmap, 0, place, h, id, &raw_full[s]);
-      }
-      if (j + 1 < n) id = page_of(base_of(j + 1) + 16 * (lane & 3));
+      if (lane < 8 && mine % per == 0)
+        tma_load_4d(sm + Sh::kRawOff + s * Sh::kBytes8 + mine * D, h2 & 1 ? &vmap : &kmap, 0,
+                    (base_of(j) + mine) & (P - 1), h, id, &raw_full[s]);
+      if (h2 & 1) id = next;
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
-      auto scores = [&](int j) {  // S of step j, both tiles
-        ok = ok && ring_wait(&kv_full[j % kKv], (uint32_t)(j / kKv) & 1u);
-        if (!ok) return;
-        tc_fence_after();
-        for (int r = 0; r < tiles; ++r) {
-          const uint32_t q = sm + Sh::kQOff + r * Sh::kQ, k = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss(tmem + r * Sh::kTile + (j & 1) * kT,
-                    sw128_desc(q + (kk >> 2) * (128 * 128) + (kk & 3) * 32),
-                    sw128_desc(k + (kk >> 2) * (kT * 128) + (kk & 3) * 32), kk != 0, kIdS);
-          umma_commit(&s_full[r][j & 1]);
-        }
+    if (n > 0) {
+      const uint32_t leader = lane == 0;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, ring_wait(bar, parity)) != 0;
       };
-      ok = ring_wait(&q_full, 0u);
-      scores(0);
+      const uint64_t qd = sw128_desc(sm + Sh::kQOff), kd = sw128_desc(sm + Sh::kOpOff);
+      const uint64_t vd = sw128_desc_mn(sm + Sh::kOpOff, kT * 128);
+      auto slot = [&](int h2) { return (uint64_t)((h2 % kOps) * Sh::kOp >> 4); };
+      auto ready = [&](int h2) { return wait(&op_full[h2 % kOps], (uint32_t)(h2 / kOps) & 1u); };
+      auto scores = [&](int j, int r) {
+        tc_fence_after();
+        const uint64_t q = qd + (uint64_t)(r * Sh::kQ >> 4), k = kd + slot(2 * j);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(leader, tmem + r * Sh::kTile, q + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                  k + (((kk >> 2) * (kT * 128) + (kk & 3) * 32) >> 4), kk != 0, kIdS);
+        umma_commit_if(leader, &s_full[r]);
+        if (r == tiles - 1) umma_commit_if(leader, &op_empty[2 * j % kOps]);
+      };
+      ok = wait(&q_full, 0u) && ready(0);
+      for (int r = 0; r < tiles && ok; ++r) scores(0, r);
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) {
-          // the other S buffer holds P of the step before: its product has to be done
-          if (j > 0) ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
-          scores(j + 1);
-        }
+        ok = ready(2 * j + 1);
         for (int r = 0; r < tiles && ok; ++r) {
-          ok = ring_wait(&p_full[r][j & 1], (uint32_t)(j >> 1) & 1u);
+          ok = wait(&p_full[r], (uint32_t)j & 1u);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp + Sh::kOp;
+          const uint64_t v = vd + slot(2 * j + 1);
 #pragma unroll
           for (int kk = 0; kk < kT / 16; ++kk)
-            umma_ts(tmem + r * Sh::kTile + 128, tmem + r * Sh::kTile + (j & 1) * kT + 8 * kk,
-                    sw128_desc_mn(v + kk * 2048, kT * 128), (j | kk) != 0, kIdO);
+            umma_ts(leader, tmem + r * Sh::kTile + kT, tmem + r * Sh::kTile + 8 * kk,
+                    v + (kk * 2048 >> 4), (j | kk) != 0, kIdO);
+          if (r == tiles - 1) umma_commit_if(leader, &op_empty[(2 * j + 1) % kOps]);
+          if (j + 1 == n) {
+            umma_commit_if(leader, &o_full[r]);
+          } else {
+            // S goes where P lies: its product has to be done (and O may be
+            // rescaled once S is there)
+            umma_commit_if(leader, &pv_done[r]);
+            ok = (r > 0 || ready(2 * j + 2)) && wait(&pv_done[r], (uint32_t)j & 1u);
+            if (ok) scores(j + 1, r);
+          }
         }
-        if (!ok) break;
-        umma_commit(&kv_empty[j % kKv]);
-        umma_commit(&pv_done);
       }
     }
-    __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // bytes to fp16.  A thread takes 16-byte chunk c of token tok; tokens that no
     // row sees become zeros, whatever lies there.
     const int e = tid - 128;
-    constexpr int kItems = kT * (D / 16) / 128;
-    int tok[kItems], ch[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      if (D == 128) {
-        // 8 neighbours: 4 chunks of a token and the other 4 of the next one, so
-        // that neither the reads nor the writes meet in a bank
-        tok[i] = (e >> 2) + 32 * (i >> 1);
-        ch[i] = (e & 3) + 4 * (((e >> 2) ^ i) & 1);
-      } else {
-        tok[i] = (e >> 2) + 32 * i;
-        ch[i] = e & 3;
-      }
-    }
-    // scales of the step's groups of 16 tokens: lane i < 4 of warp 4, the pages
+    constexpr int kItems = kT * (D / 16) / 128, kAtOnce = 4;
+    // scales of the step's groups of 16 tokens: lane i < 8 of warp 4, the pages
     // two steps and the scales one step ahead
     auto scales = [&](int id, float &ks, float &vs) {
       ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
       vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
     };
-    const bool sc = warp == 4 && lane < 4;
+    const bool sc = warp == 4 && lane < kT / 16;
     float ks = 0.0f, vs = 1.0f;
     int id = 0;
     if (sc && n > 0) {
       scales(page_of(base_of(0) + 16 * lane), ks, vs);
       if (n > 1) id = page_of(base_of(1) + 16 * lane);
     }
-    for (int j = 0; j < n; ++j) {
-      const int s = j % kRaw, base = base_of(j);
-      ok = ring_wait(&raw_full[s], (uint32_t)(j / kRaw) & 1u) &&
-           (j < kKv || ring_wait(&kv_empty[j % kKv], ((uint32_t)(j / kKv) & 1u) ^ 1u));
+    for (int h2 = 0; h2 < 2 * n; ++h2) {
+      const int s = h2 % kRaw, j = h2 >> 1, base = base_of(j);
+      ok = ring_wait(&raw_full[s], (uint32_t)(h2 / kRaw) & 1u) &&
+           (h2 < kOps || ring_wait(&op_empty[h2 % kOps], ((uint32_t)(h2 / kOps) & 1u) ^ 1u));
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
-      if (sc) {
-        s_sc[j % kKv][0][lane] = ks;
-        s_sc[j % kKv][1][lane] = __log2f(vs);
-        s_sc[j % kKv][2][lane] = __fdividef(1.0f, vs);
-        if (j + 1 < n) scales(id, ks, vs);
-        if (j + 2 < n) id = page_of(base_of(j + 2) + 16 * lane);
+      if (warp == 4 && !(h2 & 1)) {
+        // (a slot's last step has been through its softmax: the step after it
+        // has had its S, of the keys whose operand slot is free now)
+        if (sc) {
+          s_sc[j % kSc][0][lane] = ks;
+          s_sc[j % kSc][1][lane] = __log2f(vs);
+          s_sc[j % kSc][2][lane] = __fdividef(1.0f, vs);
+          if (j + 1 < n) scales(id, ks, vs);
+          if (j + 2 < n) id = page_of(base_of(j + 2) + 16 * lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[j % kSc]);
       }
       const bool whole = base + kT <= hi && (base >= lo || base + kT <= p.sinks);
-      const uint32_t raw = sm + Sh::kRawOff + s * (2 * Sh::kBytes8);
-      const uint32_t op = sm + Sh::kOpOff + (j % kKv) * 2 * Sh::kOp;
+      const uint32_t raw = sm + Sh::kRawOff + s * Sh::kBytes8;
+      const uint32_t op = sm + Sh::kOpOff + (h2 % kOps) * Sh::kOp;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        uint4 x[kItems];
+      for (int i0 = 0; i0 < kItems; i0 += kAtOnce) {
+        uint4 x[kAtOnce];
+        int tok[kAtOnce], ch[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) x[i] = lds16(raw + kv * Sh::kBytes8 + swz<D>(tok[i], ch[i]));
+        for (int i = 0; i < kAtOnce; ++i) {
+          if (D == 128) {
+            // 8 neighbours: 4 chunks of a token and the other 4 of the next one,
+            // so that neither the reads nor the writes meet in a bank
+            tok[i] = (e >> 2) + 32 * ((i0 + i) >> 1);
+            ch[i] = (e & 3) + 4 * (((e >> 2) ^ i) & 1);
+          } else {
+            tok[i] = (e >> 2) + 32 * (i0 + i);
+            ch[i] = e & 3;
+          }
+          x[i] = lds16(raw + swz<D>(tok[i], ch[i]));
+        }
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
+        for (int i = 0; i < kAtOnce; ++i) {
           if (!whole) {
             const int at = base + tok[i];
             if (!(at < hi && (at >= lo || at < p.sinks))) x[i] = make_uint4(0, 0, 0, 0);
           }
           // fp16 chunks 2 c, 2 c + 1 of the row: half c / 4
-          const uint32_t row = op + kv * Sh::kOp + (ch[i] >> 2) * (kT * 128) + tok[i] * 128;
+          const uint32_t row = op + (ch[i] >> 2) * (kT * 128) + tok[i] * 128;
           const int c = (2 * ch[i]) & 7, r7 = tok[i] & 7;
           sts16(row + ((c ^ r7) << 4), to_f16x2<I8, 0>(x[i].x), to_f16x2<I8, 1>(x[i].x),
                 to_f16x2<I8, 0>(x[i].y), to_f16x2<I8, 1>(x[i].y));
@@ -373,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&kv_full[j % kKv]);
+        mbar_arrive(&op_full[h2 % kOps]);
         mbar_arrive(&raw_empty[s]);
       }
     }
@@ -425,83 +451,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wlo = __reduce_max_sync(0xFFFFFFFFu, live ? blo : 0);
     for (int j = 0; j < n; ++j) {
       const int base = base_of(j);
-      ok = ring_wait(&s_full[r][j & 1], (uint32_t)(j >> 1) & 1u) &&
-           ring_wait(&kv_full[j % kKv], (uint32_t)(j / kKv) & 1u);  // (s_sc of the step)
+      ok = ring_wait(&s_full[r], (uint32_t)j & 1u) &&
+           ring_wait(&sc_full[j % kSc], (uint32_t)(j / kSc) & 1u);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t x[kT];
-      tmem_get(tl + (j & 1) * kT, x);
-      tmem_get(tl + (j & 1) * kT + 32, x + 32);
-      tmem_got(x);
-      tmem_got(x + 32);
-      // exponents against the reference: s * scale + log2(vs) - ref
+      const bool edge = base + kT > whi || base < wlo;  // some row of the warp does not see it whole
+      // 32 columns become exponents against the reference: s * scale + log2(vs) - ref
+      auto exponents = [&](int c, uint32_t (&x)[32]) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint64_t f = pair(s_sc[j % kKv][0][c] * qm), o = pair(s_sc[j % kKv][1][c] - ref);
+        for (int g = 0; g < 2; ++g) {
+          const uint64_t f = pair(s_sc[j % kSc][0][2 * c + g] * qm);
+          const uint64_t o = pair(s_sc[j % kSc][1][2 * c + g] - ref);
 #pragma unroll
-        for (int e = 16 * c; e < 16 * c + 16; e += 2) fma2(x[e], x[e + 1], f, o);
-      }
-      if (base + kT > whi || base < wlo) {  // some row of the warp does not see it whole
-#pragma unroll
-        for (int e = 0; e < kT; ++e) {
-          const int at = base + e;
-          if (!(at < bhi && (at >= blo || at < p.sinks))) x[e] = 0xFF800000u;  // -infinity
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) fma2(x[e], x[e + 1], f, o);
         }
-      }
-      float mx = __uint_as_float(x[0]);
+        if (edge) {
 #pragma unroll
-      for (int e = 1; e < kT; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+          for (int e = 0; e < 32; ++e) {
+            const int at = base + 32 * c + e;
+            if (!(at < bhi && (at >= blo || at < p.sinks))) x[e] = 0xFF800000u;  // -infinity
+          }
+        }
+      };
+      uint32_t x[2][32];  // one half on its way while the other is worked on
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_get(tl, x[0]);
+#pragma unroll
+      for (int c = 0; c < kT / 32; ++c) {
+        tmem_got(x[c & 1]);
+        tmem_get(tl + 32 * ((c + 1) % (kT / 32)), x[(c + 1) & 1]);  // (at the end the first again)
+        exponents(c, x[c & 1]);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            m4[q] = fmaxf(fmaxf(m4[q], __uint_as_float(x[c & 1][e + q])),
+                          __uint_as_float(x[c & 1][e + q + 4]));
+      }
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       const bool need = mx > (fresh_row ? -INFINITY : kLift + kGrow);
       if (__any_sync(0xFFFFFFFFu, need)) {
-        // a new reference: what lies in O and l counts against the old one
+        // a new reference: what lies in O and l counts against the old one (the
+        // step before is done: its product was waited for before S was computed)
         const float by = need ? mx - kLift : 0.0f;
-        const bool rescale = need && !fresh_row;
         ref += by;
-#pragma unroll
-        for (int e = 0; e < kT; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) - by);
-        if (__any_sync(0xFFFFFFFFu, rescale)) {
-          const float corr = rescale ? ex2(-by) : 1.0f;
+        if (__any_sync(0xFFFFFFFFu, need && !fresh_row)) {
+          const float corr = need && !fresh_row ? ex2(-by) : 1.0f;
           l *= corr;
-          ok = ring_wait(&pv_done, (uint32_t)(j - 1) & 1u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t y[32];
-            tmem_get(tl + 128 + 32 * c, y);
+            tmem_get(tl + kT + 32 * c, y);
             tmem_got(y);
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
-            tmem_put(tl + 128 + 32 * c, y);
+            tmem_put(tl + kT + 32 * c, y);
           }
         }
         fresh_row = fresh_row && !need;
       }
-      uint32_t pk[kT / 2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint64_t sum = 0;  // a pair of sums
+      for (int c = 0; c < kT / 32; ++c) {
+        tmem_got(x[c & 1]);
+        if (c + 1 < kT / 32) tmem_get(tl + 32 * (c + 1), x[(c + 1) & 1]);
+        exponents(c, x[c & 1]);
+        uint32_t pk[16];  // P, pairs of fp16
 #pragma unroll
-        for (int e = 16 * c; e < 16 * c + 16; e += 2) {
-          const float a = ex2(__uint_as_float(x[e])), d = ex2(__uint_as_float(x[e + 1]));
-          add2(sum, a, d);
-          const __half2 hp = __floats2half2_rn(a, d);
-          pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hp);
+        for (int g = 0; g < 2; ++g) {
+          uint64_t s2 = 0;  // a pair of sums
+#pragma unroll
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            const float a = ex2(__uint_as_float(x[c & 1][e])), d = ex2(__uint_as_float(x[c & 1][e + 1]));
+            add2(s2, a, d);
+            const __half2 hp = __floats2half2_rn(a, d);
+            pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hp);
+          }
+          l = fmaf(__uint_as_float((uint32_t)s2) + __uint_as_float((uint32_t)(s2 >> 32)),
+                   s_sc[j % kSc][2][2 * c + g], l);
         }
-        const float lo2 = __uint_as_float((uint32_t)sum), hi2 = __uint_as_float((uint32_t)(sum >> 32));
-        l = fmaf(lo2 + hi2, s_sc[j % kKv][2][c], l);
+        // over columns of S that have been read (32 c + 31 at least)
+        tmem_put(tl + 16 * c, pk);
       }
-      tmem_put(tl + (j & 1) * kT, pk);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
-      // (one barrier per buffer: a fast warp may be a step ahead of a slow one)
-      mbar_arrive(&p_full[r][j & 1]);
+      mbar_arrive(&p_full[r]);
     }
     // O: the last step's product is done
     if (n > 0 && ok) {
-      ok = ring_wait(&pv_done, (uint32_t)(n - 1) & 1u);
+      ok = ring_wait(&o_full[r], 0u);
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
     tc_fence_after();
@@ -513,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < D / 32; ++c) {
       uint32_t y[32];
       if (n > 0 && ok) {
-        tmem_get(tl + 128 + 32 * c, y);
+        tmem_get(tl + kT + 32 * c, y);
         tmem_got(y);
       }
       if (!live) continue;
@@ -555,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(Sh::kTmem)
+                 "r"(kTmem)
                  : "memory");
   }
   if (active == 1) return;

@@ -26,6 +26,16 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
                    "r"(smem_u32(bar))
                : "memory");
 }
+// the same from a warp that runs as a whole, by its leader
+__device__ __forceinline__ void umma_commit_if(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }

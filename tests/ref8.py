@@ -108,7 +108,7 @@ def attention(cache, q, table, lens, off, scale, window=0, sinks=0):
     log2 of the value scale and subtracting the maximum round twice at the size
     of |S| + 64; exp2 errs by 2^-22 relative.  A probability is then rounded to
     11 bits: 2^-11 relative, or half of fp16's smallest step, 2^-25, where the
-    largest one is held as at least 2^7; that is 2^-32 of the largest product of
+    largest one is held as at least 2^4; that is 2^-29 of the largest product of
     a probability and its page's scale, and a page's largest value is at least
     half of its format's.  Numerator and
     denominator carry these errors, the output one rounding to bf16 (2^-8)."""
@@ -149,7 +149,7 @@ def attention(cache, q, table, lens, off, scale, window=0, sinks=0):
                 lse[r, hd] = top + np.log(den)
                 es = (D + 6) * 2.0 ** -23 * env + 2 * 2.0 ** -24 * (env * 1.45 + 64) + 2.0 ** -22
                 mag = w @ np.abs(v) / den
-                small = see.sum() * 2.0 ** -31 * np.abs(v).max()
+                small = see.sum() * 2.0 ** -28 * np.abs(v).max()
                 bO[r, hd] = (2 * es + 2.0 ** -11 + 2.0 ** -20) * mag + 2.0 ** -8 * np.abs(O[r, hd]) + small
                 bl[r, hd] = es + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r, hd])
     return O, lse, bO, bl
