@@ -199,7 +199,8 @@ struct AttnShape {
   static constexpr int kPitch = D + 4;                         // floats per row of a warp's result
   static constexpr int kOut = 8 * NR * kPitch * 4;             // bytes of it
   static constexpr int kWarpOut = SHARE ? kOut : kRing;        // from one warp's to the next's
-  static constexpr int kBytes = kRing * kRings > kWarps * kWarpOut ? kRing * kRings : kWarps * kWarpOut;
+  static constexpr int kUsed = kRing * kRings > kWarps * kWarpOut ? kRing * kRings : kWarps * kWarpOut;
+  static constexpr int kBytes = kUsed > kMergeBytes ? kUsed : kMergeBytes;
   static constexpr int kPart = kRows * D + 2 * kRows;          // floats of a CTA's partial result
   static_assert(SHARE || kOut <= kRing, "a warp's result fits its ring");
 };
@@ -483,25 +484,30 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
           iv[i] = __fdividef(1.0f, vs[i]);
         }
 #pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s[i][n][e] = fmaf(s[i][n][e], ks[i] * qm[n][e & 1], lv[i]);
+        if (edge) {  // (a branch of its own: few steps take it)
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {  // tokens g and g + 8, rows 2 t and 2 t + 1
+                const int tok = base + 16 * i + 8 * (e >> 1) + g, c = e & 1;
+                if (!(tok < bound_hi[n][c] && (tok >= bound_lo[n][c] || tok < p.sinks)))
+                  s[i][n][e] = -INFINITY;
+              }
+          asm volatile("" ::: "memory");
+        }
+#pragma unroll
         for (int n = 0; n < NR; ++n) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = m[n][c];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float f = ks[i] * qm[n][c];
-#pragma unroll
-              for (int d = 0; d < 2; ++d) {  // tokens g and g + 8
-                float &x = s[i][n][2 * d + c];
-                x = fmaf(x, f, lv[i]);
-                if (edge) {
-                  const int tok = base + 16 * i + 8 * d + g;
-                  if (!(tok < bound_hi[n][c] && (tok >= bound_lo[n][c] || tok < p.sinks)))
-                    x = -INFINITY;
-                }
-                v = fmaxf(v, x);
-              }
-            }
+            float v = fmaxf(fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c])), m[n][c]);
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
@@ -552,13 +558,17 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
               const uint2 x = lds8(vb + swz<D>(tok, g >> 1) + 8 * (g & 1));
               w[e][0] = x.x; w[e][1] = x.y;
             }
-            if (edge) {  // what lies in tokens that no row sees must not count
-              const int at = base + tok;
+          }
+          if (edge) {  // what lies in tokens that no row sees must not count
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = base + 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
               if (!(at < hi && (at >= lo || at < p.sinks))) {
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q) w[e][q] = 0;
               }
             }
+            asm volatile("" ::: "memory");
           }
 #pragma unroll
           for (int q = 0; q < D / 32; ++q)
@@ -680,23 +690,9 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const float *up = p.part + (int64_t)unit * p.splits * Sh::kPart;
-  for (int e = tid; e < urows * (D / 4); e += Sh::kThreads) {
-    const int row = e / (D / 4), d = e % (D / 4) * 4;
-    float mx = -INFINITY;
-    for (int s = 0; s < active; ++s)
-      mx = fmaxf(mx, __ldcg(up + (int64_t)s * Sh::kPart + Sh::kRows * D + row));
-    const float safe = mx == -INFINITY ? 0.0f : mx;
-    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float den = 0.0f;
-    for (int s = 0; s < active; ++s) {
-      const float *q = up + (int64_t)s * Sh::kPart;
-      const float f = ex2(__ldcg(q + Sh::kRows * D + row) - safe);
-      add(num, f, __ldcg(reinterpret_cast<const float4 *>(q + row * D + d)));
-      den = fmaf(f, __ldcg(q + Sh::kRows * D + Sh::kRows + row), den);
-    }
-    write_out(row, d, num, den, mx);
-  }
+  merge_parts<D, Sh::kRows, Sh::kThreads>(p, p.part + (int64_t)unit * p.splits * Sh::kPart, active,
+                                          urows, u0, row0, h, kLift,
+                                          reinterpret_cast<float *>(smem));
 }
 
 // ---------------------------------------------------------------------------
@@ -747,25 +743,32 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
   return HYB_OK;
 }
 
-// The split of a unit's steps: enough CTAs to fill the GPU (a few times over
-// where the CTAs are small), none below 4 steps nor, for units of few rows that
-// do not fill it alone, above 32 (1024 tokens: sequences of different lengths
-// then end at about the same time).  Only units that are split have tickets,
-// which lie at a fixed place whatever the call's shape, so that calls of
-// different shapes can share a workspace.
-constexpr int kMinChunk = 4, kMaxChunk = 32;
+// The split of a unit's steps over CTAs: as many CTAs as fit the GPU at a time
+// (3 per SM for units of 8 rows, 2 for 16 and 64, 1 for 256; a third more where
+// all the work is small and the CTAs' start counts), none below 4 steps.  Where
+// units alone fill the GPU, and there for units of few rows only, a CTA has at
+// most 40 steps (else 64), so that sequences of different lengths end at about
+// the same time: 32 sequences of 1024 to 8192 tokens took 49.6 us with 48 steps
+// and 46.9 us with 32, one of 65536 45 us with 32 and 36 us with 40.  Only units
+// that are split have tickets, which lie at a fixed place whatever the call's
+// shape, so that calls of different shapes can share a workspace.
+constexpr int kMinChunk = 4;
 constexpr int kShareRows = 64;  // most rows of mma.sync units
 constexpr int kTickets = 2048;
 int step_of(int rows) { return rows == kPrefillRows ? kPrefillStep : kStep; }
 void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, int *chunk) {
   const int step = step_of(rows);
   const int64_t steps = (tokens + step - 1) / step + 1;  // a range may start inside a step
-  const int64_t fill = rows == kPrefillRows ? sms : 4ll * sms;  // CTAs wanted
-  const bool many = units >= (rows <= 16 ? 2 * fill : fill) || units > kTickets;
+  const int64_t fit = rows == kPrefillRows ? 1 : rows > 8 ? 2 : units * steps < 32ll * sms ? 4 : 3;
+  const int64_t fill = fit * sms;
+  const bool many = units >= (rows <= 16 ? 8ll * sms : fill) || units > kTickets;
   const int64_t want = many ? 1 : (fill + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
   if (c < kMinChunk) c = kMinChunk;
-  if (c > kMaxChunk && !many && rows <= 16) c = kMaxChunk;
+  const int64_t top = units >= sms ? 40 : 64;
+  if (c > top && !many && rows <= 16) c = top;
+  const int64_t most = kMergeRows / rows;  // parts that the last CTA can add
+  if ((steps + c - 1) / c > most) c = (steps + most - 1) / most;
   c = (c + kMinChunk - 1) / kMinChunk * kMinChunk;
   *chunk = (int)c;
   *splits = (int)((steps + c - 1) / c);

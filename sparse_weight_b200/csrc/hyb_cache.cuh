@@ -107,6 +107,70 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// A unit's last CTA adds the parts of its `active` CTAs in their order: first all
+// maxima and sums (kMergeRows of them at most, which bounds the splits) come to
+// shared memory at once and become each part's weight, then the rows are summed
+// with several loads on their way.  `lift`: what the stored maximum has to be
+// lowered by to be P's reference.
+constexpr int kMergeRows = 4096;
+constexpr int kMergeBytes = 8 * kMergeRows;
+template <int D, int ROWS, int THREADS>
+__device__ __forceinline__ void merge_parts(const AttnParams &p, const float *up, int active,
+                                            int urows, int64_t u0, int64_t row0, int h, float lift,
+                                            float *sm) {
+  constexpr int kPart = ROWS * D + 2 * ROWS;
+  const int tid = threadIdx.x, G = p.group;
+  float *sm_m = sm, *sm_l = sm + kMergeRows;  // [active][urows]
+  for (int e = tid; e < active * urows; e += THREADS) {
+    const int s = e / urows, row = e - s * urows;
+    const float *q = up + (int64_t)s * kPart + ROWS * D + row;
+    sm_m[e] = __ldcg(q);
+    sm_l[e] = __ldcg(q + ROWS);
+  }
+  __syncthreads();
+  for (int row = tid; row < urows; row += THREADS) {
+    float mx = -INFINITY, den = 0.0f;
+    for (int s = 0; s < active; ++s) mx = fmaxf(mx, sm_m[s * urows + row]);
+    const float safe = mx == -INFINITY ? 0.0f : mx;
+    for (int s = 0; s < active; ++s) {
+      const float f = ex2(sm_m[s * urows + row] - safe);
+      den = fmaf(f, sm_l[s * urows + row], den);
+      sm_m[s * urows + row] = f;
+    }
+    const int64_t rr = u0 + row;
+    if (p.lse)
+      p.lse[(row0 + rr / G) * p.ldl + h * G + rr % G] =
+          den != 0.0f ? (safe - lift + log2f(den)) * 0.693147180559945309f : -INFINITY;
+    sm_l[row] = den != 0.0f ? 1.0f / den : 0.0f;  // (the row's own first sum is used up)
+  }
+  __syncthreads();
+  for (int e = tid; e < urows * (D / 4); e += THREADS) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    const float *q = up + row * D + d;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < active; s0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < active) x[s] = __ldcg(reinterpret_cast<const float4 *>(q + (int64_t)(s0 + s) * kPart));
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if (s0 + s >= active) break;
+        const float f = sm_m[(s0 + s) * urows + row];
+        num.x = fmaf(f, x[s].x, num.x);
+        num.y = fmaf(f, x[s].y, num.y);
+        num.z = fmaf(f, x[s].z, num.z);
+        num.w = fmaf(f, x[s].w, num.w);
+      }
+    }
+    const int64_t rr = u0 + row;
+    const float r = sm_l[row];
+    *reinterpret_cast<uint2 *>(p.O + (row0 + rr / G) * p.ldo + (h * G + rr % G) * p.hso + d) =
+        make_uint2(f32_to_bf16_rne(num.x * r) | ((uint32_t)f32_to_bf16_rne(num.y * r) << 16),
+                   f32_to_bf16_rne(num.z * r) | ((uint32_t)f32_to_bf16_rne(num.w * r) << 16));
+  }
+}
+
 // Attention of units of 256 query rows on the tensor cores
 // (hyb_cache_prefill.cu); p.chunk counts steps of 128 tokens there.
 constexpr int kPrefillRows = 256, kPrefillStep = 128;

@@ -609,35 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  const float *up = p.part + (int64_t)unit * p.splits * Sh::kPart;
-  for (int e = tid; e < urows * (D / 4); e += kThreads) {
-    const int row = e / (D / 4), d = e % (D / 4) * 4;
-    float mx = -INFINITY;
-    for (int s = 0; s < active; ++s)
-      mx = fmaxf(mx, __ldcg(up + (int64_t)s * Sh::kPart + kPrefillRows * D + row));
-    const float safe = mx == -INFINITY ? 0.0f : mx;
-    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float den = 0.0f;
-    for (int s = 0; s < active; ++s) {
-      const float *q = up + (int64_t)s * Sh::kPart;
-      const float f = ex2(__ldcg(q + kPrefillRows * D + row) - safe);
-      const float4 x = __ldcg(reinterpret_cast<const float4 *>(q + row * D + d));
-      num.x = fmaf(f, x.x, num.x);
-      num.y = fmaf(f, x.y, num.y);
-      num.z = fmaf(f, x.z, num.z);
-      num.w = fmaf(f, x.w, num.w);
-      den = fmaf(f, __ldcg(q + kPrefillRows * D + kPrefillRows + row), den);
-    }
-    const int64_t rr = u0 + row;
-    const int i = (int)(rr / G), hd = h * G + (int)(rr % G);
-    const float inv = den != 0.0f ? 1.0f / den : 0.0f;
-    *reinterpret_cast<uint2 *>(p.O + (row0 + i) * p.ldo + hd * p.hso + d) =
-        make_uint2(f32_to_bf16_rne(num.x * inv) | ((uint32_t)f32_to_bf16_rne(num.y * inv) << 16),
-                   f32_to_bf16_rne(num.z * inv) | ((uint32_t)f32_to_bf16_rne(num.w * inv) << 16));
-    if (d == 0 && p.lse)
-      p.lse[(row0 + i) * p.ldl + hd] =
-          den != 0.0f ? (mx + log2f(den)) * 0.693147180559945309f : -INFINITY;
-  }
+  merge_parts<D, kPrefillRows, kThreads>(p, p.part + (int64_t)unit * p.splits * Sh::kPart, active,
+                                         urows, u0, row0, h, 0.0f, reinterpret_cast<float *>(smem));
 }
 
 template <int D, bool I8>
