@@ -820,8 +820,8 @@ int launch_shape(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &
                  cudaStream_t st) {
   using Sh = AttnShape<D, NR, SHARE>;
   const int dyn = Sh::kBytes + 1024;
-  if (cudaFuncSetAttribute(cache_attention_kernel<D, I8, NR, SHARE>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(reinterpret_cast<const void *>(cache_attention_kernel<D, I8, NR, SHARE>), dyn, done) != HYB_OK)
     return HYB_ERR_CUDA;
   if (units * p.splits > INT32_MAX) return HYB_ERR_UNSUPPORTED;
   return launch_dependent(cache_attention_kernel<D, I8, NR, SHARE>,
@@ -920,22 +920,21 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   int qtiles, sms, splits, chunk;
   rc = attn_units(C, S->batch, S->max_new, heads, &units, &qtiles);
   if (rc != HYB_OK) return rc;
-  const size_t need = hyb_cache_attention_workspace_bytes(C, S->batch, S->max_new, S->max_pages,
-                                                          heads);
-  if (!ws || need == 0 || ws_bytes < need) return HYB_ERR_WORKSPACE;
-  if ((uintptr_t)ws % 256 != 0) return HYB_ERR_ALIGNMENT;
+  if (!ws) return HYB_ERR_WORKSPACE;
   rc = device_sm_count(&sms);
   if (rc != HYB_OK) return rc;
-  // tokens that one unit sees at most
-  const int64_t all = (int64_t)S->max_pages * C->page_size;
   const int rows = unit_rows((int64_t)S->max_new * (heads / C->kv_heads));
+  const int64_t all = (int64_t)S->max_pages * C->page_size;
+  int full_splits, full_chunk;
+  split_plan(units, rows, all, sms, &full_splits, &full_chunk);
+  if (ws_bytes < attn_bytes(C, units, rows, full_splits)) return HYB_ERR_WORKSPACE;
+  if ((uintptr_t)ws % 256 != 0) return HYB_ERR_ALIGNMENT;
+  // tokens that one unit sees at most
   int64_t tokens = all;
   if (window) {
     const int64_t span = (int64_t)window + rows + (int64_t)sinks + 2 * step_of(rows);
     if (span < tokens) tokens = span;
   }
-  int full_splits, full_chunk;
-  split_plan(units, rows, all, sms, &full_splits, &full_chunk);
   split_plan(units, rows, tokens, sms, &splits, &chunk);
   if (splits > full_splits) {  // never more than the workspace holds
     splits = full_splits;

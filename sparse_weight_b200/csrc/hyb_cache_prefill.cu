@@ -617,8 +617,8 @@ template <int D, bool I8>
 int launch(const AttnParams &p, const CUtensorMap &km, const CUtensorMap &vm, int64_t units,
            cudaStream_t st) {
   const int dyn = PShape<D>::kBytes + 1024;
-  if (cudaFuncSetAttribute(cache_attention_prefill_kernel<D, I8>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(reinterpret_cast<const void *>(cache_attention_prefill_kernel<D, I8>), dyn, done) != HYB_OK)
     return HYB_ERR_CUDA;
   if (units * p.splits > INT32_MAX) return HYB_ERR_UNSUPPORTED;
   return launch_dependent(cache_attention_prefill_kernel<D, I8>,

@@ -342,8 +342,8 @@ int launch_gemm(const Fp8Params &p, int C, cudaStream_t st) {
   if (rc == HYB_OK) rc = encode_bytes(p.W, p.k, p.n, p.ldw, BN, &wmap);
   if (rc != HYB_OK) return rc;
   const int dyn = Sh::kRing + 1024;
-  if (cudaFuncSetAttribute(fp8_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           dyn) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(reinterpret_cast<const void *>(fp8_gemm_kernel<BN>), dyn, done) != HYB_OK)
     return HYB_ERR_CUDA;
   return launch_dependent(fp8_gemm_kernel<BN>, dim3((unsigned)(tiles * C), (unsigned)toks), Sh::kThreads, dyn, C, st, p,
                           xmap, wmap);
@@ -569,8 +569,8 @@ int launch_decode(const Fp8Params &p, int C, cudaStream_t st) {
   if (rc == HYB_OK) rc = encode_bytes(p.X, p.k, p.m, p.ldx, kDecodeTokens, &xmap);
   if (rc != HYB_OK) return rc;
   const int dyn = Sh::kBytes + 1024;
-  if (cudaFuncSetAttribute(fp8_decode_kernel<BN>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, dyn) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(reinterpret_cast<const void *>(fp8_decode_kernel<BN>), dyn, done) != HYB_OK)
     return HYB_ERR_CUDA;
   return launch_dependent(fp8_decode_kernel<BN>, dim3((unsigned)(tiles * C)), kDecodeThreads, dyn, C, st, p,
                           xmap, wmap);

@@ -9,6 +9,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "hyb.h"
@@ -206,6 +207,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   return encode;
+}
+
+// Raises a kernel's shared-memory limit, once per device (`done`: a bit per
+// device, one word per kernel).
+inline int allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return HYB_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return HYB_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return HYB_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_release);
+  return HYB_OK;
 }
 
 // A launch as a programmatic dependent, in clusters of C CTAs along x.

@@ -681,26 +681,27 @@ _NO_SCOPE = contextlib.nullcontext()
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _scope(device, stream):
-    """Make ``device`` current and ``stream`` (or the device's current stream)
-    the one that new tensors belong to; returns (stream handle, context).
-    Outputs and workspaces made inside a call are then allocated in the order
-    of the stream that uses them."""
+def _scope(index, stream):
+    """Make device ``index`` current and ``stream`` (or the device's current
+    stream) the one that new tensors belong to; returns (stream handle,
+    context).  Outputs and workspaces made inside a call are then allocated in
+    the order of the stream that uses them."""
     if stream is not None:
         return stream.cuda_stream, torch.cuda.stream(stream)
-    index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         return _raw_stream(index), _NO_SCOPE
-    return _raw_stream(index), torch.cuda.device(device)
+    return _raw_stream(index), torch.cuda.device(index)
 
 
-def _on_device(fn, device, *tensors):
-    """Every tensor lives on the CUDA device of the first."""
-    if device.type != "cuda":
-        raise ValueError(f"{fn}: tensors must live on a CUDA device")
+def _device_of(fn, first, *tensors):
+    """The index of the CUDA device that every tensor lives on."""
+    index = first.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{fn}: tensors on {device} and {t.device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{fn}: tensors on {first.device} and {t.device}")
+    if index < 0:
+        raise ValueError(f"{fn}: tensors must live on a CUDA device")
+    return index
 
 
 def _want(fn, ok, what):
@@ -733,6 +734,7 @@ class Fp8Matrix:
             self.n, self.k, self.q.data_ptr(),
             self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
             self.scale.data_ptr(), max(self.scale.stride(0), kb)))
+        object.__setattr__(self, "_ref", ctypes.byref(self._struct))
 
     def struct(self) -> HybFp8Matrix:
         return self._struct
@@ -752,29 +754,31 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
     multiple of 16 bytes apart, as the products need them."""
     f = "quant_fp8"
     xdt = _QUANT_TYPES.get(X.dtype)
-    if xdt is None:
-        raise ValueError(f"{f}: X must be bf16 or fp32")
-    _want(f, X.dim() == 2, "X must be [rows][cols]")
+    if xdt is None or X.dim() != 2:
+        raise ValueError(f"{f}: X must be bf16 or fp32 [rows][cols]")
     rows, cols = X.shape
-    ldx = X.stride(0)
-    _want(f, rows > 0 and cols > 0, "X must not be empty")
-    _want(f, cols == 1 or X.stride(1) == 1, "rows of X must be contiguous")
-    _want(f, block_rows in (1, 128), "block_rows must be 1 or 128")
-    dev = X.device
-    _on_device(f, dev, ws)
-    handle, scope = _scope(dev, stream)
+    ldx, one = X.stride()
+    if rows < 1 or cols < 1 or (one != 1 and cols > 1):
+        raise ValueError(f"{f}: X must not be empty and its rows must be contiguous")
+    if block_rows != 1 and block_rows != 128:
+        raise ValueError(f"{f}: block_rows must be 1 or 128")
+    index = _device_of(f, X, ws)
+    handle, scope = _scope(index, stream)
     ld, cb = -(-cols // 16) * 16, -(-cols // 128)
+    dev = X.device
     with scope:
-        q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=dev)
-        if ld != cols:
-            q = q[:, :cols]
+        if ld == cols:
+            q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+        else:
+            q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.float8_e4m3fn, device=dev)
         s = torch.empty((-(-rows // block_rows), cb), dtype=torch.float32, device=dev)
         if ws is None:
             ws = new_workspace(fp8_quant_workspace_bytes(), dev)
         rc = lib().hyb_fp8_quant(rows, cols, X.data_ptr(), ldx if ldx > cols else cols, xdt,
                                  block_rows, q.data_ptr(), ld, s.data_ptr(), cb, ws.data_ptr(),
                                  ws.numel(), handle)
-    _check("hyb_fp8_quant", rc)
+    if rc:
+        raise HybError("hyb_fp8_quant", rc)
     return q, s
 
 
@@ -787,7 +791,7 @@ def pack_fp8(W: torch.Tensor, ws: torch.Tensor = None, stream=None,
     128 x 128 blocks).  With ``check`` the call synchronises and raises HybError
     on a NaN or infinite weight."""
     if ws is None:
-        with _scope(W.device, stream)[1]:
+        with _scope(_device_of("pack_fp8", W), stream)[1]:
             ws = new_workspace(fp8_quant_workspace_bytes(), W.device)
     q, s = quant_fp8(W, 128, ws, stream)
     if check:
@@ -812,36 +816,41 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
     if X.dim() == 1:
         X = X.view(1, -1)
     n, k = A.n, A.k
-    _want(f, X.dim() == 2 and X.shape[1] == k and X.shape[0] > 0, "X must be [m][k]")
+    if X.dim() != 2 or X.shape[1] != k or X.shape[0] < 1:
+        raise ValueError(f"{f}: X must be [m][k]")
     m = X.shape[0]
-    ldx = X.stride(0)
-    _want(f, k == 1 or X.stride(1) == 1, "rows of X must be contiguous")
+    ldx, one = X.stride()
+    if one != 1 and k > 1:
+        raise ValueError(f"{f}: rows of X must be contiguous")
     if xs is None:
-        _want(f, X.dtype == torch.bfloat16, "X must be bf16, or e4m3 with xs")
+        if X.dtype != torch.bfloat16:
+            raise ValueError(f"{f}: X must be bf16, or e4m3 with xs")
+        xdt, sp, lds = HYB_BF16, None, 0
     else:
-        _want(f, X.dtype == torch.float8_e4m3fn, "X with xs must be float8_e4m3fn")
-        _want(f, xs.dtype == torch.float32 and xs.shape == (m, A.scale.shape[1])
-              and (xs.shape[1] == 1 or xs.stride(1) == 1), "xs must be fp32 [m][ceil(k / 128)]")
+        kb = -(-k // 128)
+        if X.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"{f}: X with xs must be float8_e4m3fn")
+        if xs.dtype != torch.float32 or xs.shape != (m, kb) or (xs.stride(1) != 1 and kb > 1):
+            raise ValueError(f"{f}: xs must be fp32 [m][ceil(k / 128)]")
+        xdt, sp, lds = HYB_E4M3, xs.data_ptr(), max(xs.stride(0), kb)
     ytype = _OUT_TYPES.get(ydt)
-    _want(f, ytype is not None, "ydt must be HYB_F32 or HYB_BF16")
-    if Y is not None:
-        _want(f, Y.shape == (m, n) and (n == 1 or Y.stride(1) == 1) and Y.dtype == ytype,
-              "Y must be [m][n] in ydt")
-    dev = X.device
-    _on_device(f, dev, A.q, A.scale, xs, Y, ws)
-    handle, scope = _scope(dev, stream)
+    if ytype is None:
+        raise ValueError(f"{f}: ydt must be HYB_F32 or HYB_BF16")
+    if Y is not None and (Y.shape != (m, n) or (Y.stride(1) != 1 and n > 1) or Y.dtype != ytype):
+        raise ValueError(f"{f}: Y must be [m][n] in ydt")
+    index = _device_of(f, X, A.q, A.scale, xs, Y, ws)
+    handle, scope = _scope(index, stream)
     with scope:
         if Y is None:
-            Y = torch.empty((m, n), dtype=ytype, device=dev)
+            Y = torch.empty((m, n), dtype=ytype, device=X.device)
         if ws is None:
-            ws = new_workspace(fp8_workspace_bytes(m, n, k), dev)
+            ws = new_workspace(fp8_workspace_bytes(m, n, k), X.device)
         # a single row's stride says nothing
-        rc = lib().hyb_fp8_matmul(
-            ctypes.byref(A._struct), m, X.data_ptr(), ldx if m > 1 else -(-k // 16) * 16,
-            HYB_BF16 if xs is None else HYB_E4M3, None if xs is None else xs.data_ptr(),
-            0 if xs is None else max(xs.stride(0), xs.shape[1]), Y.data_ptr(),
-            Y.stride(0) if m > 1 else n, ydt, flags, ws.data_ptr(), ws.numel(), handle)
-    _check("hyb_fp8_matmul", rc)
+        rc = lib().hyb_fp8_matmul(A._ref, m, X.data_ptr(), ldx if m > 1 else -(-k // 16) * 16, xdt,
+                                  sp, lds, Y.data_ptr(), Y.stride(0) if m > 1 else n, ydt, flags,
+                                  ws.data_ptr(), ws.numel(), handle)
+    if rc:
+        raise HybError("hyb_fp8_matmul", rc)
     return Y
 
 
@@ -881,6 +890,7 @@ class Cache:
             self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
             self.v_scale.data_ptr(), HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages,
             heads, size, dim, sp, sh, st))
+        object.__setattr__(self, "_ref", ctypes.byref(self._struct))
 
     @property
     def page_size(self) -> int:
@@ -900,23 +910,25 @@ def new_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
 
 
 def _sequences(f, rows, page_table, lens, off, max_new):
-    _want(f, page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table must be int32 "
-          "[batch][pages]")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        raise ValueError(f"{f}: page_table must be int32 [batch][pages]")
     batch, pages = page_table.shape
     stride, one = page_table.stride()
-    _want(f, pages == 1 or one == 1, "rows of page_table must be contiguous")
-    _want(f, lens.dtype == torch.int32 and lens.shape == (batch,) and lens.is_contiguous(),
-          "lens must be int32 [batch]")
+    if one != 1 and pages > 1:
+        raise ValueError(f"{f}: rows of page_table must be contiguous")
+    if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
+        raise ValueError(f"{f}: lens must be int32 [batch]")
+    at = None
     if off is None:
         if max_new is None and batch and rows % batch == 0:
             max_new = rows // batch
-        _want(f, max_new is not None and rows == batch * max_new,
-              "without off every sequence has max_new rows")
-        at = None
+        if max_new is None or rows != batch * max_new:
+            raise ValueError(f"{f}: without off every sequence has max_new rows")
     else:
-        _want(f, off.dtype == torch.int32 and off.shape == (batch + 1,) and off.is_contiguous(),
-              "off must be int32 [batch + 1]")
-        _want(f, max_new is not None, "off needs max_new")
+        if off.dtype != torch.int32 or off.shape != (batch + 1,) or not off.is_contiguous():
+            raise ValueError(f"{f}: off must be int32 [batch + 1]")
+        if max_new is None:
+            raise ValueError(f"{f}: off needs max_new")
         at = off.data_ptr()
     return HybSequences(batch, max_new, rows, lens.data_ptr(), at, page_table.data_ptr(), pages,
                         stride if stride > pages else pages)
@@ -944,21 +956,23 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
     [batch + 1]: the sequences' rows (None: max_new rows each)."""
     f = "cache_append"
     c = C._struct
-    rows, _, ldk, hsk = _heads(f, K, c.kv_heads, c.head_dim, "K")
-    rows_v, _, ldv, hsv = _heads(f, V, c.kv_heads, c.head_dim, "V")
-    _want(f, rows == rows_v, "K and V must have the same rows")
-    dev = C.k.device
-    _on_device(f, dev, K, V, page_table, lens, off, ws)
+    heads, dim = c.kv_heads, c.head_dim
+    rows, _, ldk, hsk = _heads(f, K, heads, dim, "K")
+    rows_v, _, ldv, hsv = _heads(f, V, heads, dim, "V")
+    if rows != rows_v:
+        raise ValueError(f"{f}: K and V must have the same rows")
+    index = _device_of(f, C.k, K, V, page_table, lens, off, ws)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
     if rows == 0:
         return
-    handle, scope = _scope(dev, stream)
+    handle, scope = _scope(index, stream)
     with scope:
         if ws is None:
-            ws = new_workspace(cache_append_workspace_bytes(), dev)
-        rc = lib().hyb_cache_append(ctypes.byref(c), ctypes.byref(seq), K.data_ptr(), ldk, hsk,
+            ws = new_workspace(cache_append_workspace_bytes(), C.k.device)
+        rc = lib().hyb_cache_append(C._ref, ctypes.byref(seq), K.data_ptr(), ldk, hsk,
                                     V.data_ptr(), ldv, hsv, ws.data_ptr(), ws.numel(), handle)
-    _check("hyb_cache_append", rc)
+    if rc:
+        raise HybError("hyb_cache_append", rc)
 
 
 def cache_attention_workspace_bytes(C: Cache, batch: int, heads: int, max_new: int,
@@ -986,15 +1000,16 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     c = C._struct
     dim = c.head_dim
     rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
-    dev = C.k.device
-    _on_device(f, dev, Q, page_table, lens, off, out, ws)
+    index = _device_of(f, C.k, Q, page_table, lens, off, out, ws)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
     if out is not None:
         out_rows, _, ldo, hso = _heads(f, out, heads, dim, "out")
-        _want(f, out_rows == rows, "out must have Q's shape")
+        if out_rows != rows:
+            raise ValueError(f"{f}: out must have Q's shape")
     else:
         ldo, hso = heads * dim, dim
-    handle, scope = _scope(dev, stream)
+    handle, scope = _scope(index, stream)
+    dev = Q.device
     with scope:
         if out is None:
             out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
@@ -1005,9 +1020,10 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
                 ws = new_workspace(cache_attention_workspace_bytes(
                     C, seq.batch, heads, seq.max_new, seq.max_pages * c.page_size), dev)
             rc = lib().hyb_cache_attention(
-                ctypes.byref(c), ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo,
-                hso, lse.data_ptr() if return_lse else None, heads, heads,
+                C._ref, ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso,
+                lse.data_ptr() if return_lse else None, heads, heads,
                 dim ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),
                 handle)
-    _check("hyb_cache_attention", rc)
+    if rc:
+        raise HybError("hyb_cache_attention", rc)
     return (out, lse) if return_lse else out
