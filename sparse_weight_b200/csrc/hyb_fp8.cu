@@ -16,6 +16,59 @@
 namespace hyb {
 namespace {
 
+// 8 consecutive values of a row as they lie in memory (no value is looked at, so
+// that several loads are on their way at once); those at or past `left` are
+// zeros.  `vec`: the rows start on 16 bytes (else they are read one by one).
+template <bool F32>
+struct Raw {
+  uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load_raw(const void *X, int64_t off, int left, bool vec) {
+  Raw<F32> r;
+  r.w[0] = make_uint4(0, 0, 0, 0);
+  if constexpr (F32) r.w[1] = make_uint4(0, 0, 0, 0);
+  const float *xf = static_cast<const float *>(X) + off;
+  const uint16_t *xb = static_cast<const uint16_t *>(X) + off;
+  if (left >= 8 && vec) {
+    if constexpr (F32) {
+      r.w[0] = ld_dep16(xf);
+      r.w[1] = ld_dep16(xf + 4);
+    } else {
+      r.w[0] = ld_dep16(xb);
+    }
+  } else if (left > 0) {
+    uint32_t e[F32 ? 8 : 4] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) {
+        if constexpr (F32)
+          e[i] = __float_as_uint(ld_dep(xf + i));
+        else
+          e[i >> 1] |= (uint32_t) * static_cast<const volatile uint16_t *>(xb + i) << (16 * (i & 1));
+      }
+    r.w[0] = make_uint4(e[0], e[1], e[2], e[3]);
+    if constexpr (F32) r.w[1] = make_uint4(e[4], e[5], e[6], e[7]);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void unpack(const Raw<F32> &r, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+    const uint32_t w[4] = {r.w[h].x, r.w[h].y, r.w[h].z, r.w[h].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        v[4 * h + i] = __uint_as_float(w[i]);
+      } else {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    }
+  }
+}
+
 // 8 bytes of a row; those at or past `left` are not written
 __device__ __forceinline__ void store8(uint8_t *Q, int64_t off, int left, uint2 w) {
   if (left >= 8) {
@@ -26,40 +79,106 @@ __device__ __forceinline__ void store8(uint8_t *Q, int64_t off, int left, uint2 
   }
 }
 
-// One scale per row and 128 columns.  A half-warp owns one block at a time (16
-// lanes x 8 values: 16 bytes of bf16 per lane, 8 bytes written).
+// The largest |x| of 8 values as its bits: magnitudes order as integers, an
+// infinity or a NaN above every finite value.
 template <bool F32>
-__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(int64_t rows, int64_t cols,
+__device__ __forceinline__ uint32_t top_bits(const Raw<F32> &r) {
+  if constexpr (F32) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      a = max(max(max(a, r.w[h].x & 0x7FFFFFFFu), max(r.w[h].y & 0x7FFFFFFFu, r.w[h].z & 0x7FFFFFFFu)),
+              r.w[h].w & 0x7FFFFFFFu);
+    return a;
+  } else {  // two values at a time, joined by top_of
+    return __vmaxu2(__vmaxu2(r.w[0].x & 0x7FFF7FFFu, r.w[0].y & 0x7FFF7FFFu),
+                    __vmaxu2(r.w[0].z & 0x7FFF7FFFu, r.w[0].w & 0x7FFF7FFFu));
+  }
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t top_max(uint32_t a, uint32_t b) {
+  return F32 ? max(a, b) : __vmaxu2(a, b);
+}
+template <bool F32>
+__device__ __forceinline__ uint32_t top_of(uint32_t a) {
+  return F32 ? a : max(a << 16, a & 0xFFFF0000u);
+}
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// 8 values times inv as e4m3
+template <bool F32>
+__device__ __forceinline__ uint2 to_e4m3(const Raw<F32> &r, float inv) {
+  float v[8];
+  unpack(r, v);
+  return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// One scale per row and 128 columns.  A warp owns 2 kSeg blocks of a row, a half-
+// warp every other one of them (16 lanes x 8 values: 16 bytes of bf16 per lane,
+// 8 bytes written), with all of them on their way at once.  The instructions
+// count here as much as the bytes: the largest values are compared as bits, two
+// at a time, and a lane makes one of its half-warp's 2 kSeg divisions.
+template <bool F32, int kSeg>
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(int64_t rows, int64_t cols64,
                                                              const void *X, int64_t ldx,
                                                              uint8_t *Q, int64_t ldq,
                                                              float *scale, int64_t lds,
-                                                             int64_t cb, bool vec, uint32_t *status) {
+                                                             int segs, bool vec, uint32_t *status) {
+  static_assert(kSeg <= 8, "two divisions per block over 16 lanes");
   // dependents start once the preceding kernel has ended: a product behind this
   // kernel may then read W at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 15;
-  const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const unsigned half = 0xFFFFu << (threadIdx.x & 16);
-  if (unit >= rows * cb) return;
-  const int64_t row = unit / cb, blk = unit - row * cb;
-  const int64_t col = blk * kBlk + lane * 8;
-  const int left = (int)max((int64_t)0, min((int64_t)8, cols - col));
-  float v[8];
-  load8<F32>(X, row * ldx + col, left, vec, v);
-  float a = 0.0f;
+  const int cols = (int)cols64;
+  const int l16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int row = (int)(unit / segs);
+  if (row >= rows) return;
+  const int blk0 = (int)(unit - (int64_t)row * segs) * (2 * kSeg) + half;
+  const int col0 = blk0 * kBlk + l16 * 8;
+  const int64_t x0 = row * ldx, q0 = row * ldq;
+  Raw<F32> raw[kSeg];
+#pragma unroll
+  for (int j = 0; j < kSeg; ++j)
+    raw[j] = load_raw<F32>(X, x0 + col0 + 2 * kBlk * j, cols - (col0 + 2 * kBlk * j), vec);
+  float a[kSeg];
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax_finite(v[i], a, bad);
+  for (int j = 0; j < kSeg; ++j) {
+    uint32_t m = top_bits(raw[j]);
 #pragma unroll
-  for (int o = 8; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(half, a, o));
-  a = fmaxf(a, kMinAmax);
-  const float inv = __fdiv_rn(kE4m3Max, a);
-  uint2 w;
-  w.x = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  w.y = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-  store8(Q, row * ldq + col, left, w);
-  if (lane == 0) scale[row * lds + blk] = __fdiv_rn(a, kE4m3Max);
+    for (int o = 8; o; o >>= 1) m = top_max<F32>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    m = top_of<F32>(m);
+    a[j] = __uint_as_float(m);
+    if (__any_sync(0xFFFFFFFFu, m >= kInfBits)) {  // only the finite values count
+      float v[8];
+      unpack(raw[j], v);
+      a[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax_finite(v[i], a[j], bad);
+#pragma unroll
+      for (int o = 8; o; o >>= 1) a[j] = fmaxf(a[j], __shfl_xor_sync(0xFFFFFFFFu, a[j], o));
+    }
+    a[j] = fmaxf(a[j], kMinAmax);
+  }
+  // lane i < kSeg: 448 / a of block i; lane kSeg + i: a / 448 of it
+  float mine = a[0];
+#pragma unroll
+  for (int j = 1; j < kSeg; ++j)
+    if (l16 % kSeg == j) mine = a[j];
+  const bool is_scale = (l16 / kSeg) & 1;
+  const float quot = __fdiv_rn(is_scale ? mine : kE4m3Max, is_scale ? kE4m3Max : mine);
+  if (l16 >= kSeg && l16 < 2 * kSeg) {
+    const int blk = blk0 + 2 * (l16 - kSeg);
+    if (blk * kBlk < cols) scale[row * lds + blk] = quot;
+  }
+#pragma unroll
+  for (int j = 0; j < kSeg; ++j) {
+    const float inv = __shfl_sync(0xFFFFFFFFu, quot, j, 16);
+    const int col = col0 + 2 * kBlk * j;
+    store8(Q, q0 + col, cols - col, to_e4m3(raw[j], inv));
+  }
   if (bad) atomicOr(status, kStatusNaN);
 }
 
@@ -77,20 +196,29 @@ __global__ void __launch_bounds__(256) fp8_quant_blocks_kernel(int64_t rows, int
   const int64_t col = (int64_t)blockIdx.x * kBlk + lane * 8;
   const int64_t row0 = (int64_t)blockIdx.y * kBlk + r16;
   const int left = (int)max((int64_t)0, min((int64_t)8, cols - col));
-  float v[8][8];
-  float a = 0.0f;
-  bool bad = false;
+  Raw<F32> raw[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t row = row0 + 16 * j;
-    load8<F32>(X, row * ldx + col, row < rows ? left : 0, vec, v[j]);
+    raw[j] = load_raw<F32>(X, row * ldx + col, row < rows ? left : 0, vec);
   }
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int j = 0; j < 8; ++j) m = top_max<F32>(m, top_bits(raw[j]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax_finite(v[j][i], a, bad);
+  for (int o = 16; o; o >>= 1) m = top_max<F32>(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float a = __uint_as_float(top_of<F32>(m));
+  bool bad = false;
+  if (!(a <= 3.402823466e38f)) {  // only the finite values count
+    a = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      float v[8];
+      unpack(raw[j], v);
+      for (int i = 0; i < 8; ++i) amax_finite(v[i], a, bad);
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  }
   if ((threadIdx.x & 31) == 0) s_a[threadIdx.x >> 5] = a;
   __syncthreads();
   a = kMinAmax;
@@ -100,10 +228,7 @@ __global__ void __launch_bounds__(256) fp8_quant_blocks_kernel(int64_t rows, int
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int64_t row = row0 + 16 * j;
-    uint2 w;
-    w.x = e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv);
-    w.y = e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv);
-    if (row < rows) store8(Q, row * ldq + col, left, w);
+    if (row < rows) store8(Q, row * ldq + col, left, to_e4m3(raw[j], inv));
   }
   if (threadIdx.x == 0) scale[(int64_t)blockIdx.y * lds + blockIdx.x] = __fdiv_rn(a, kE4m3Max);
   if (bad) atomicOr(status, kStatusNaN);
@@ -115,11 +240,18 @@ int quant_launch(int64_t rows, int64_t cols, const void *X, int64_t ldx, hyb_dty
   const int64_t cb = (cols + kBlk - 1) / kBlk;
   const bool vec = (uintptr_t)X % 16 == 0 && ldx % (xdt == HYB_F32 ? 4 : 8) == 0;
   if (block_rows == 1) {
-    const int64_t ctas = (rows * cb + 15) / 16;
+    // Where one block per half-warp fits the GPU at a time, that is the shortest
+    // way (16 x 4096 in bf16: 1.6 us, 2.4 us with four); else four hide the loads
+    // and share the divisions.
+    const bool small = rows * cb <= 2 * 32 * 148;
+    const int per = 2 * (small ? 1 : 4);  // blocks per warp
+    const int64_t segs = (cb + per - 1) / per;
+    const int64_t ctas = (rows * segs + 7) / 8;
     if (ctas > INT32_MAX) return HYB_ERR_UNSUPPORTED;
     return launch_dependent(
-        xdt == HYB_F32 ? fp8_quant_rows_kernel<true> : fp8_quant_rows_kernel<false>,
-        dim3((unsigned)ctas), 256, 0, 1, st, rows, cols, X, ldx, Q, ldq, scale, lds, cb, vec,
+        xdt == HYB_F32 ? (small ? fp8_quant_rows_kernel<true, 1> : fp8_quant_rows_kernel<true, 4>)
+                       : (small ? fp8_quant_rows_kernel<false, 1> : fp8_quant_rows_kernel<false, 4>),
+        dim3((unsigned)ctas), 256, 0, 1, st, rows, cols, X, ldx, Q, ldq, scale, lds, (int)segs, vec,
         status);
   }
   const int64_t rb = (rows + kBlk - 1) / kBlk;

@@ -34,42 +34,6 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
 
-// 8 consecutive values of a row as fp32; those at or past `left` read as zero.
-// `vec`: the rows start on 16 bytes (else they are read value by value).
-template <bool F32>
-__device__ __forceinline__ void load8(const void *X, int64_t off, int left, bool vec,
-                                      float (&v)[8]) {
-  if (left >= 8 && vec) {
-    if constexpr (F32) {
-      const float *p = static_cast<const float *>(X) + off;
-      const uint4 a = ld_dep16(p), b = ld_dep16(p + 4);
-      v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-      v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-      v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
-      v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-    } else {
-      const uint4 r = ld_dep16(static_cast<const uint16_t *>(X) + off);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.0f;
-      if (i < left) {
-        if constexpr (F32)
-          v[i] = ld_dep(static_cast<const float *>(X) + off + i);
-        else
-          v[i] = __uint_as_float((uint32_t) static_cast<const volatile uint16_t *>(X)[off + i] << 16);
-      }
-    }
-  }
-}
-
 // One product: W [n][k] and X [m][k] e4m3 (X bf16 where the small kernel
 // quantises it itself), their scales, and Y.
 struct Fp8Params {

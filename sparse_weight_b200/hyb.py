@@ -767,11 +767,10 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
     ld, cb = -(-cols // 16) * 16, -(-cols // 128)
     dev = X.device
     with scope:
-        if ld == cols:
-            q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
-        else:
-            q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.float8_e4m3fn, device=dev)
-        s = torch.empty((-(-rows // block_rows), cb), dtype=torch.float32, device=dev)
+        # (empty_strided: 1 us less per tensor than empty)
+        q = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.float8_e4m3fn, device=dev)
+        s = torch.empty_strided((-(-rows // block_rows), cb), (cb, 1), dtype=torch.float32,
+                                device=dev)
         if ws is None:
             ws = new_workspace(fp8_quant_workspace_bytes(), dev)
         rc = lib().hyb_fp8_quant(rows, cols, X.data_ptr(), ldx if ldx > cols else cols, xdt,
@@ -842,7 +841,7 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
     handle, scope = _scope(index, stream)
     with scope:
         if Y is None:
-            Y = torch.empty((m, n), dtype=ytype, device=X.device)
+            Y = torch.empty_strided((m, n), (n, 1), dtype=ytype, device=X.device)
         if ws is None:
             ws = new_workspace(fp8_workspace_bytes(m, n, k), X.device)
         # a single row's stride says nothing
@@ -1012,8 +1011,10 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     dev = Q.device
     with scope:
         if out is None:
-            out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev) if return_lse else None
+            out = torch.empty_strided((rows, heads, dim), (ldo, dim, 1), dtype=torch.bfloat16,
+                                      device=dev)
+        lse = torch.empty_strided((rows, heads), (heads, 1), dtype=torch.float32,
+                                  device=dev) if return_lse else None
         rc = HYB_OK
         if rows:
             if ws is None:
