@@ -727,6 +727,9 @@ class Fp8Matrix:
         _want(f, (self.k == 1 or self.q.stride(1) == 1)
               and (self.scale.shape[1] == 1 or self.scale.stride(1) == 1),
               "rows of q and scale must be contiguous")
+        _want(f, (self.n == 1 or self.q.stride(0) >= self.k)
+              and (self.scale.shape[0] == 1 or self.scale.stride(0) >= self.scale.shape[1]),
+              "rows of q and scale must not overlap (an expanded tensor has to be copied)")
         # the C struct, made once: the fields cannot be assigned again
         # (a single row's stride says nothing: at least the row's length)
         kb = self.scale.shape[1]
@@ -760,6 +763,11 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
     ldx, one = X.stride()
     if rows < 1 or cols < 1 or (one != 1 and cols > 1):
         raise ValueError(f"{f}: X must not be empty and its rows must be contiguous")
+    if rows == 1:
+        ldx = cols  # a single row's stride says nothing
+    elif ldx < cols:
+        raise ValueError(f"{f}: rows of X must not overlap "
+                         "(an expanded tensor has to be copied)")
     if block_rows != 1 and block_rows != 128:
         raise ValueError(f"{f}: block_rows must be 1 or 128")
     index = _device_of(f, X, ws)
@@ -773,8 +781,8 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
                                 device=dev)
         if ws is None:
             ws = new_workspace(fp8_quant_workspace_bytes(), dev)
-        rc = lib().hyb_fp8_quant(rows, cols, X.data_ptr(), ldx if ldx > cols else cols, xdt,
-                                 block_rows, q.data_ptr(), ld, s.data_ptr(), cb, ws.data_ptr(),
+        rc = lib().hyb_fp8_quant(rows, cols, X.data_ptr(), ldx, xdt, block_rows,
+                                 q.data_ptr(), ld, s.data_ptr(), cb, ws.data_ptr(),
                                  ws.numel(), handle)
     if rc:
         raise HybError("hyb_fp8_quant", rc)
@@ -831,7 +839,10 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
             raise ValueError(f"{f}: X with xs must be float8_e4m3fn")
         if xs.dtype != torch.float32 or xs.shape != (m, kb) or (xs.stride(1) != 1 and kb > 1):
             raise ValueError(f"{f}: xs must be fp32 [m][ceil(k / 128)]")
-        xdt, sp, lds = HYB_E4M3, xs.data_ptr(), max(xs.stride(0), kb)
+        xdt, sp, lds = HYB_E4M3, xs.data_ptr(), xs.stride(0) if m > 1 else kb
+        if lds < kb:
+            raise ValueError(f"{f}: rows of xs must not overlap "
+                             "(an expanded tensor has to be copied)")
     ytype = _OUT_TYPES.get(ydt)
     if ytype is None:
         raise ValueError(f"{f}: ydt must be HYB_F32 or HYB_BF16")
@@ -915,6 +926,11 @@ def _sequences(f, rows, page_table, lens, off, max_new):
     stride, one = page_table.stride()
     if one != 1 and pages > 1:
         raise ValueError(f"{f}: rows of page_table must be contiguous")
+    if batch <= 1:
+        stride = pages  # a single row's stride says nothing
+    elif stride < pages:
+        raise ValueError(f"{f}: rows of page_table must not overlap "
+                         "(an expanded tensor has to be copied)")
     if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
         raise ValueError(f"{f}: lens must be int32 [batch]")
     at = None
@@ -930,7 +946,7 @@ def _sequences(f, rows, page_table, lens, off, max_new):
             raise ValueError(f"{f}: off needs max_new")
         at = off.data_ptr()
     return HybSequences(batch, max_new, rows, lens.data_ptr(), at, page_table.data_ptr(), pages,
-                        stride if stride > pages else pages)
+                        stride)
 
 
 def _heads(f, x, heads, dim, what):
@@ -960,8 +976,8 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
     rows_v, _, ldv, hsv = _heads(f, V, heads, dim, "V")
     if rows != rows_v:
         raise ValueError(f"{f}: K and V must have the same rows")
-    index = _device_of(f, C.k, K, V, page_table, lens, off, ws)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
+    index = _device_of(f, C.k, K, V, page_table, lens, off, ws)
     if rows == 0:
         return
     handle, scope = _scope(index, stream)
@@ -999,8 +1015,8 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     c = C._struct
     dim = c.head_dim
     rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
-    index = _device_of(f, C.k, Q, page_table, lens, off, out, ws)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
+    index = _device_of(f, C.k, Q, page_table, lens, off, out, ws)
     if out is not None:
         out_rows, _, ldo, hso = _heads(f, out, heads, dim, "out")
         if out_rows != rows:

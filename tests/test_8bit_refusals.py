@@ -156,3 +156,32 @@ def test_binding_checks():
     for bad in (dict(Q=q.float()), dict(Q=q[:, :, :32]), dict(Q=q[:1])):
         with pytest.raises(ValueError):
             hyb.cache_attention(C, bad["Q"], t, lens)
+
+
+def test_expanded_rows_are_refused():
+    """Rows that lie on one another (expand) would be read past their tensor's end; one row may have any stride."""
+    e4 = torch.zeros(4, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    a = hyb.Fp8Matrix(4, 128, e4, torch.zeros(1, 1))
+    q300 = torch.zeros(300, 128, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="overlap"):
+        hyb.Fp8Matrix(300, 128, q300, torch.zeros(1, 1).expand(3, 1))
+    with pytest.raises(ValueError, match="overlap"):
+        hyb.Fp8Matrix(300, 128, q300[:1].view(torch.uint8).expand(300, 128), torch.zeros(3, 1))
+    for block_rows in (1, 128):
+        for x in (torch.zeros(1, 128).expand(5, 128), torch.zeros(200).as_strided((3, 128), (16, 1))):
+            with pytest.raises(ValueError, match="overlap"):
+                hyb.quant_fp8(x, block_rows)
+    with pytest.raises(ValueError, match="overlap"):
+        hyb.matmul_fp8(a, e4, xs=torch.zeros(1, 1).expand(4, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        hyb.matmul_fp8(a, e4[:1], xs=torch.zeros(1, 1).expand(1, 1))
+    kv, s = torch.zeros(3, 2, 16, 64, dtype=torch.int8), torch.zeros(3, 2)
+    C = hyb.Cache(kv, kv, s, s)
+    q, lens = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.ones(2, dtype=torch.int32)
+    for t in (torch.zeros(1, 3, dtype=torch.int32).expand(2, 3), torch.zeros(8, dtype=torch.int32).as_strided((2, 3), (2, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            hyb.cache_attention(C, q, t, lens)
+        with pytest.raises(ValueError, match="overlap"):
+            hyb.cache_append(C, q[:, :2], q[:, 2:], t, lens)
+    with pytest.raises(ValueError, match="CUDA"):
+        hyb.cache_attention(C, q[:1], torch.zeros(1, 1, dtype=torch.int32).expand(1, 3).contiguous()[:, :3], lens[:1])
