@@ -534,8 +534,11 @@ HYB_API size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t b
  *      softmax's sum of exponentials, or NULL
  * heads is a multiple of kv_heads; window >= 0 (0 = none), sinks >= 0.
  * fp32 accumulation and softmax statistics; the probabilities are rounded to
- * 11 bits for the second product.  A cached NaN counts where a query of the
- * sequence sees its token; tokens that none sees are not used.  Tickets and
+ * 11 bits for the second product.  Value scales below 2^-64, 0 among them, count
+ * as 2^-64 there.  A cached NaN counts where a query of the sequence sees its
+ * token; tokens that none sees are not used, nor are the table entries and the
+ * scales of pages of which none sees a token (they need not be valid).  O must
+ * not overlap Q.  Tickets and
  * partial results live in the workspace, zeroed once before its first use and
  * from then on used by hyb_cache_attention only (calls of different shapes may
  * share one that is large enough for each); results are deterministic. */

@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   const int first = len - fresh;
 
   // the unit's visible tokens: [0, sinks) and [lo, hi); a query at place q sees t <= q
-  int na, nb0, nsteps;
+  int na, nb0, nsteps, ulo, uhi;
   {
     const int i0 = (int)(u0 / G), i1 = (int)((u0 + urows - 1) / G);
-    const int uhi = len == 0 ? 0 : first + i1 + 1;
-    const int ulo = p.window ? max(0, first + i0 - p.window + 1) : 0;
+    uhi = len == 0 ? 0 : first + i1 + 1;
+    ulo = p.window ? max(0, first + i0 - p.window + 1) : 0;
     na = p.window ? (min(p.sinks, uhi) + kStep - 1) / kStep : 0;  // steps of the sinks
     nb0 = ulo / kStep;
     if (nb0 <= na) na = nb0 = 0;
@@ -301,14 +301,16 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
     __syncwarp();
 
   // pages, 16 steps at a time: lane l holds step l / 2's page of tokens
-  // 16 (l & 1) .. (the same page twice where pages hold a step)
+  // 16 (l & 1) .. (the same page twice where pages hold a step); -1 where no row
+  // sees a token of that half (or step)
+  const int P = 1 << p.s.page_shift;
   const int32_t *table = p.s.table + b * p.s.table_stride;
   auto load_ids = [&](int w0) {
     const int j = w0 + (lane >> 1);
-    int id = 0;
+    int id = -1;
     if (j < mine) {
-      const int64_t tok = base_of(j) + 16 * (lane & 1);
-      if (tok < len) {
+      const int tok = base_of(j) + (P < kStep ? 16 * (lane & 1) : 0);
+      if (seen(tok, min(P, kStep), ulo, uhi, p.sinks)) {
         id = ld_dep(table + (tok >> p.s.page_shift));
         if (id < 0 || id >= p.num_pages) {
           atomicOr(p.status, kStatusBadSeq);
@@ -318,8 +320,9 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
     }
     return id;
   };
-  const int P = 1 << p.s.page_shift;
   auto issue = [&](int j, int id0, int id1) {  // one lane: step j's boxes into its slot
+    id0 = max(id0, 0);  // (what no row sees is masked, whatever lies there)
+    id1 = max(id1, 0);
     const int s = j % NS;
     const uint32_t dst = ring32 + s * (2 * kBox);
     const int place = base_of(j) & (P - 1);
@@ -351,10 +354,7 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   float o[MT][NR][4];
   float m[NR][2], l[NR][2];
   if (computes) {
-    auto load_scales = [&](int id, float &ks, float &vs) {
-      ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
-      vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
-    };
+    auto load_scales = [&](int id, float &ks, float &vs) { page_scales(p, id, h, ks, vs); };
     int id_cur = load_ids(0), id_nxt = load_ids(16);
     float ks_cur, vs_cur, ks_nxt, vs_nxt;
     load_scales(id_cur, ks_cur, vs_cur);

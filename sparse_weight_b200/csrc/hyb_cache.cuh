@@ -61,6 +61,28 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// whether a unit that sees tokens [0, sinks) and [lo, hi), up to hi, sees one of
+// tok .. tok + n - 1
+__device__ __forceinline__ bool seen(int tok, int n, int lo, int hi, int sinks) {
+  return tok < hi && (tok + n > lo || tok < sinks);
+}
+
+// A page's scales of head h.  The kernels work with the logarithm and the
+// reciprocal of the value scale, so one below 2^-64 (a page of zeros may have 0)
+// counts as 2^-64: its values are then below 2^-55.  Where no row sees the page
+// (id -1) whatever its scales hold must not count.
+__device__ __forceinline__ void page_scales(const AttnParams &p, int id, int h, float &ks,
+                                            float &vs) {
+  constexpr float kLeast = 1.0f / 18446744073709551616.0f;
+  ks = 0.0f;
+  vs = 1.0f;
+  if (id >= 0) {
+    ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
+    vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
+    if (vs >= 0.0f && vs < kLeast) vs = kLeast;
+  }
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             int z, int w, uint64_t *bar) {
   asm volatile(

@@ -240,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const int32_t *table = p.s.table + b * p.s.table_stride;
-  // page of a token that exists; page 0 (whose values are masked) otherwise
+  // page of a token's box; -1 where no row sees a token of the box
+  const int per = min(1 << p.s.page_shift, 32);  // tokens of a box
   auto page_of = [&](int tok) {
-    int id = 0;
-    if (tok < len) {
+    int id = -1;
+    if (seen(tok & ~(per - 1), per, lo, hi, p.sinks)) {
       id = ld_dep(table + (tok >> p.s.page_shift));
       if (id < 0 || id >= p.num_pages) {
         atomicOr(p.status, kStatusBadSeq);
@@ -261,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // lane i < 8: tokens 16 i .. of the step
     const int P = 1 << p.s.page_shift;
-    const int per = min(P, 32);  // tokens of a box
     const int mine = 16 * (lane & 7);
     int id = n > 0 ? page_of(base_of(0) + mine) : 0, next = 0;
     for (int h2 = 0; h2 < 2 * n; ++h2) {  // keys, then values of each step
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane < 8 && mine % per == 0)
         tma_load_4d(sm + Sh::kRawOff + s * Sh::kBytes8 + mine * D, h2 & 1 ? &vmap : &kmap, 0,
-                    (base_of(j) + mine) & (P - 1), h, id, &raw_full[s]);
+                    (base_of(j) + mine) & (P - 1), h, max(id, 0), &raw_full[s]);  // (-1: masked)
       if (h2 & 1) id = next;
     }
   } else if (warp == 1) {
@@ -330,13 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kItems = kT * (D / 16) / 128, kAtOnce = 4;
     // scales of the step's groups of 16 tokens: lane i < 8 of warp 4, the pages
     // two steps and the scales one step ahead
-    auto scales = [&](int id, float &ks, float &vs) {
-      ks = ld_dep(p.k_scale + (int64_t)id * p.kv_heads + h);
-      vs = ld_dep(p.v_scale + (int64_t)id * p.kv_heads + h);
-    };
+    auto scales = [&](int id, float &ks, float &vs) { page_scales(p, id, h, ks, vs); };
     const bool sc = warp == 4 && lane < kT / 16;
     float ks = 0.0f, vs = 1.0f;
-    int id = 0;
+    int id = -1;
     if (sc && n > 0) {
       scales(page_of(base_of(0) + 16 * lane), ks, vs);
       if (n > 1) id = page_of(base_of(1) + 16 * lane);

@@ -354,3 +354,60 @@ def test_bad_sequences_are_flagged(i):
     hyb.cache_append(C, kv.to(dev()), kv.to(dev()), *args(bad), off=dev32(bad["off"]), max_new=3, ws=ws)
     assert _flags(ws) == hyb.STATUS_BAD_SEQ
     assert torch.equal(C.k[4:], before[0][4:]) and torch.equal(C.v_scale[4:], before[3][4:])
+
+
+def behind_a_page(C, k_scale, v_scale):
+    """The same cache behind one more page of zeros with these scales; page p becomes p + 1."""
+    kv = [torch.cat([torch.zeros_like(x.view(torch.uint8)[:1]), x.view(torch.uint8)]).view(x.dtype) for x in (C.k, C.v)]
+    sc = [torch.cat([torch.full_like(x[:1], s), x]) for x, s in ((C.k_scale, k_scale), (C.v_scale, v_scale))]
+    return hyb.Cache(kv[0], kv[1], sc[0], sc[1])
+
+
+@pytest.mark.parametrize("scales", [(0.0, 0.0), (float("nan"), float("nan")), (float("inf"), float("inf"))])
+@pytest.mark.parametrize("i", range(len(ATT)))
+def test_attention_pages_of_no_sequence(i, scales):
+    """A page that no sequence holds (page 0 of a fresh cache, say) has no part in any result, whatever its scales."""
+    lens, new, heads, kvh, dim, size, type_ = ATT[i]
+    C, table, off = setup(lens, new, kvh, dim, size, type_, seed=i)
+    q = queries(int(off[-1]), heads, dim, i)
+    for kw in ({}, dict(window=21, sinks=3)):
+        o, lse = hyb.cache_attention(behind_a_page(C, *scales), q.to(dev()), dev32(table + 1), dev32(lens),
+                                     off=dev32(off), max_new=max(new), return_lse=True, **kw)
+        check_attention(C, table, lens, off, q, o, lse, **kw)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (40, 17), (100, 0)])
+@pytest.mark.parametrize("i", [2, 5, 6, 11, 12, 14])
+def test_attention_pages_behind_the_window(i, window, sinks):
+    """Table entries of pages that no query sees are not used: a program may give those pages back."""
+    lens, new, heads, kvh, dim, size, type_ = ATT[i]
+    C, table, off = setup(lens, new, kvh, dim, size, type_, seed=i)
+    q = queries(int(off[-1]), heads, dim, i)
+    ws = hyb.new_workspace(hyb.cache_attention_workspace_bytes(C, len(lens), heads, max(new), table.shape[1] * size), dev())
+    kw = dict(window=window, sinks=sinks)
+    given = table.copy()
+    for b, t in enumerate(lens):
+        lowest = t - new[b] - window + 1
+        for j in range(given.shape[1]):
+            if j * size >= sinks and (j + 1) * size <= lowest:
+                given[b, j] = -1
+    o, lse = hyb.cache_attention(C, q.to(dev()), dev32(given), dev32(lens), off=dev32(off), max_new=max(new),
+                                 return_lse=True, ws=ws, **kw)
+    assert hyb.check_status(ws) == 0
+    check_attention(C, table, lens, off, q, o, lse, **kw)
+
+
+@pytest.mark.parametrize("i", [2, 5, 9, 11, 12, 15])
+def test_attention_zero_scales(i):
+    """Pages whose scale is 0 (a page of zeros, as some quantisers write it) count with values of 0."""
+    lens, new, heads, kvh, dim, size, type_ = ATT[i]
+    C, table, off = setup(lens, new, kvh, dim, size, type_, seed=i, poison=False)
+    q = queries(int(off[-1]), heads, dim, i)
+    g = torch.Generator().manual_seed(i)
+    for x in (C.k_scale, C.v_scale):
+        x.copy_(torch.where(torch.rand(x.shape, generator=g) < 0.3, 0.0, x.cpu()))
+    o, lse = hyb.cache_attention(C, q.to(dev()), dev32(table), dev32(lens), off=dev32(off), max_new=max(new), return_lse=True)
+    # scales below 2^-64 count as 2^-64: values of at most 448 * 2^-64
+    O, L, bO, bl = ref8.attention(host_cache(C), q.double().numpy(), table, lens, off, dim ** -0.5)
+    assert (np.abs(o.double().cpu().numpy() - O) <= bO + 448 * 2.0 ** -64 * (1 + 2.0 ** -8)).all()
+    assert (np.abs(lse.double().cpu().numpy() - L) <= bl).all()
