@@ -755,17 +755,19 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
 constexpr int kMinChunk = 4;
 constexpr int kShareRows = 64;  // most rows of mma.sync units
 constexpr int kTickets = 2048;
+constexpr int kLeastTop = 40;
+int most_per_sm(int rows) { return rows == kPrefillRows ? 1 : rows > 8 ? 2 : 4; }
 int step_of(int rows) { return rows == kPrefillRows ? kPrefillStep : kStep; }
 void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, int *chunk) {
   const int step = step_of(rows);
   const int64_t steps = (tokens + step - 1) / step + 1;  // a range may start inside a step
-  const int64_t fit = rows == kPrefillRows ? 1 : rows > 8 ? 2 : units * steps < 32ll * sms ? 4 : 3;
+  const int64_t fit = rows == 8 && units * steps >= 32ll * sms ? 3 : most_per_sm(rows);
   const int64_t fill = fit * sms;
   const bool many = units >= (rows <= 16 ? 8ll * sms : fill) || units > kTickets;
   const int64_t want = many ? 1 : (fill + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
   if (c < kMinChunk) c = kMinChunk;
-  const int64_t top = units >= sms ? 40 : 64;
+  const int64_t top = units >= sms ? kLeastTop : 64;
   if (c > top && !many && rows <= 16) c = top;
   const int64_t most = kMergeRows / rows;  // parts that the last CTA can add
   if ((steps + c - 1) / c > most) c = (steps + most - 1) / most;
@@ -777,6 +779,7 @@ void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, i
 // Query rows (of one head and sequence) per unit: 8 or 16 in a CTA that splits
 // the tokens over its warps, 64 in one whose warps have 16 each, 256 on the
 // 5th-generation tensor cores.
+int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 int unit_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= kShareRows ? 64 : kPrefillRows; }
 
 int attn_units(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t heads, int64_t *units,
@@ -790,11 +793,34 @@ int attn_units(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t heads
   return HYB_OK;
 }
 
-// workspace: header, tickets, partial results
+// Workspace: header, tickets, partial results.  Enough for every call of at most
+// these sizes, fewer tokens or units of fewer rows being split further: where
+// units are split, units x splits is below 2 x `fill` (units < fill then, and
+// splits <= fill / units + 1), or, for chunks of kLeastTop steps and more, at most
+// that many splits of the units there can be.
 constexpr size_t kPartOffset = kHeaderBytes + 4 * kTickets;
-size_t attn_bytes(const hyb_cache *C, int64_t units, int rows, int splits) {
-  return kPartOffset +
-         (splits > 1 ? (size_t)units * splits * (rows * C->head_dim + 2 * rows) * 4 : 0);
+size_t attn_bytes(const hyb_cache *C, int32_t batch, int32_t max_new, int32_t max_pages,
+                  int32_t heads, int sms) {
+  const int64_t group = heads / C->kv_heads, all = max_new * group;
+  const int64_t tokens = (int64_t)max_pages * C->page_size;
+  int64_t floats = 0;
+  for (int rows : {8, 16, kShareRows, kPrefillRows}) {
+    if (rows < unit_rows(group) || rows > unit_rows(all)) continue;
+    const int64_t qt = rows == kPrefillRows ? (all + rows - 1) / rows : 1;
+    const int64_t units = (int64_t)batch * C->kv_heads * qt;
+    const int64_t steps = (tokens + step_of(rows) - 1) / step_of(rows) + 1;
+    auto splits = [&](int64_t c) { return min64((steps + c - 1) / c, kMergeRows / rows); };
+    int64_t parts = 2ll * most_per_sm(rows) * sms;
+    if (rows <= 16) {
+      const int64_t top = min64(units, min64(8ll * sms, kTickets)) * splits(kLeastTop);
+      if (top > parts) parts = top;
+    }
+    if (splits(kMinChunk) == 1) parts = 0;
+    parts = min64(parts, units * splits(kMinChunk));
+    const int64_t f = parts * (rows * C->head_dim + 2 * rows);
+    if (f > floats) floats = f;
+  }
+  return kPartOffset + 4 * (size_t)floats;
 }
 
 int encode_pages(const hyb_cache *C, const uint8_t *base, CUtensorMap *map) {
@@ -890,12 +916,10 @@ size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch, in
                                            int32_t max_pages, int32_t heads) {
   if (cache_check(C) != HYB_OK || max_pages < 1) return 0;
   int64_t units;
-  int qtiles, sms, splits, chunk;
+  int qtiles, sms;
   if (attn_units(C, batch, max_new, heads, &units, &qtiles) != HYB_OK) return 0;
   if (device_sm_count(&sms) != HYB_OK) return 0;
-  const int rows = unit_rows((int64_t)max_new * (heads / C->kv_heads));
-  split_plan(units, rows, (int64_t)max_pages * C->page_size, sms, &splits, &chunk);
-  return attn_bytes(C, units, rows, splits);
+  return attn_bytes(C, batch, max_new, max_pages, heads, sms);
 }
 
 int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16_t *Q, int64_t ldq,
@@ -924,22 +948,16 @@ int hyb_cache_attention(const hyb_cache *C, const hyb_sequences *S, const uint16
   rc = device_sm_count(&sms);
   if (rc != HYB_OK) return rc;
   const int rows = unit_rows((int64_t)S->max_new * (heads / C->kv_heads));
-  const int64_t all = (int64_t)S->max_pages * C->page_size;
-  int full_splits, full_chunk;
-  split_plan(units, rows, all, sms, &full_splits, &full_chunk);
-  if (ws_bytes < attn_bytes(C, units, rows, full_splits)) return HYB_ERR_WORKSPACE;
+  if (ws_bytes < attn_bytes(C, S->batch, S->max_new, S->max_pages, heads, sms))
+    return HYB_ERR_WORKSPACE;
   if ((uintptr_t)ws % 256 != 0) return HYB_ERR_ALIGNMENT;
   // tokens that one unit sees at most
-  int64_t tokens = all;
+  int64_t tokens = (int64_t)S->max_pages * C->page_size;
   if (window) {
     const int64_t span = (int64_t)window + rows + (int64_t)sinks + 2 * step_of(rows);
     if (span < tokens) tokens = span;
   }
   split_plan(units, rows, tokens, sms, &splits, &chunk);
-  if (splits > full_splits) {  // never more than the workspace holds
-    splits = full_splits;
-    chunk = full_chunk;
-  }
   p.Q = Q;
   p.ldq = ldq;
   p.hsq = hsq;

@@ -46,7 +46,7 @@ class AttentionBlock:
         weights = (wq, wk, wv, wo)
         packed = [w for w in weights if isinstance(w, hyb.Packed)]
         eight = [w for w in weights if isinstance(w, hyb.Fp8Matrix)]
-        self._ws_skinny = self._ws_prefill = self._ws_fp8 = None
+        self._ws_skinny = self._ws_prefill = self._ws_fp8 = self._ws_quant = None
         if packed:
             self._ws_skinny = hyb.new_workspace(
                 max(hyb.workspace_bytes(w, b) for w in packed
@@ -61,8 +61,8 @@ class AttentionBlock:
             self._ws_quant = hyb.new_workspace(hyb.fp8_quant_workspace_bytes(), dev)
         self._ws_append = hyb.new_workspace(hyb.cache_append_workspace_bytes(), dev)
         self._ws_attention = hyb.new_workspace(
-            max(hyb.cache_attention_workspace_bytes(cache, b, heads, m, max_pages * cache.page_size)
-                for b in range(1, max_batch + 1) for m in {1, max_new}), dev)
+            hyb.cache_attention_workspace_bytes(cache, max_batch, heads, max_new,
+                                                max_pages * cache.page_size), dev)
 
     def _product(self, w: Weight, x: torch.Tensor, xs=None, xq=None) -> torch.Tensor:
         if isinstance(w, hyb.Fp8Matrix):
@@ -77,12 +77,16 @@ class AttentionBlock:
              off: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
              rotate: Optional[Callable] = None) -> torch.Tensor:
         """One step: x bf16 [rows][k] holds the new tokens of all sequences,
-        lens their lengths with them (see hyb.cache_append).  ``rotate(q, k)``
+        lens their lengths with them (see hyb.cache_append); max_new is the most
+        of one sequence (by default rows / batch, with off the block's).  ``rotate(q, k)``
         may return position-dependent q [rows][heads][dim] and k
         [rows][kv_heads][dim].  Returns bf16 [rows][wo.n]."""
         rows = x.shape[0]
         batch, pages = page_table.shape
-        new = max_new if max_new is not None else rows // max(batch, 1)
+        if max_new is not None:
+            new = max_new
+        else:  # with off, any sequence may have as many as the block allows
+            new = rows // max(batch, 1) if off is None else self.max_new
         if rows > self.max_rows or batch > self.max_batch or pages > self.max_pages \
                 or new > self.max_new:
             raise ValueError("AttentionBlock: the step is larger than the block was made for")
@@ -102,7 +106,7 @@ class AttentionBlock:
 
     def check(self) -> None:
         """Synchronise and raise if a kernel of the steps so far flagged a problem."""
-        for ws in (self._ws_skinny, self._ws_prefill, self._ws_fp8, self._ws_append,
-                   self._ws_attention):
+        for ws in (self._ws_skinny, self._ws_prefill, self._ws_fp8, self._ws_quant,
+                   self._ws_append, self._ws_attention):
             if ws is not None:
                 hyb.check_status(ws)

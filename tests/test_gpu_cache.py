@@ -411,3 +411,23 @@ def test_attention_zero_scales(i):
     O, L, bO, bl = ref8.attention(host_cache(C), q.double().numpy(), table, lens, off, dim ** -0.5)
     assert (np.abs(o.double().cpu().numpy() - O) <= bO + 448 * 2.0 ** -64 * (1 + 2.0 ** -8)).all()
     assert (np.abs(lse.double().cpu().numpy() - L) <= bl).all()
+
+
+def test_attention_workspace_of_the_largest_step():
+    """A workspace sized for the largest step serves smaller ones, with the results of one of their own."""
+    rng = np.random.default_rng(5)
+    for kvh, group, size in ((2, 4, 16), (8, 1, 32), (1, 20, 64)):
+        C = layout(3, kvh, size, 64, torch.int8, "pht", dev())
+        need = lambda b, n, pg: hyb.cache_attention_workspace_bytes(C, b, kvh * group, n, pg * size)  # noqa: E731
+        for _ in range(300):
+            B, N, W = (int(x) for x in np.exp(rng.uniform(0, np.log([64, 200, 500]))))
+            top = need(B, N, W)
+            assert need(int(rng.integers(1, B + 1)), int(rng.integers(1, N + 1)), int(rng.integers(1, W + 1))) <= top
+    lens, new = [200] * 11, [12] * 11
+    C, table, off = setup(lens, new, 2, 64, 16, "e4m3", seed=1)
+    q = queries(132, 8, 64, 1).to(dev())
+    ws = hyb.new_workspace(hyb.cache_attention_workspace_bytes(C, 13, 8, 21, 22 * 16), dev())
+    for n, rows in ((12, 132), (1, 11), (3, 33)):
+        a = (C, q[:rows], dev32(table), dev32(lens))
+        assert torch.equal(hyb.cache_attention(*a, ws=ws), hyb.cache_attention(*a))
+    assert hyb.check_status(ws) == 0

@@ -99,3 +99,42 @@ def test_step_refuses_what_it_was_not_made_for():
         blk.step(x, dev32(np.zeros((2, 5))), dev32([1, 1]))
     with pytest.raises(ValueError):
         decode.AttentionBlock(blk.wk, blk.wk, blk.wv, blk.wo, HEADS, blk.cache, 2, 4)
+
+
+@pytest.mark.parametrize("batch,new,width", [(11, 12, 22), (13, 1, 5), (1, 21, 22), (4, 3, 9)])
+def test_smaller_steps_fit(batch, new, width):
+    """A block serves every step within its sizes, as one made for just that step does."""
+    B, N, W = 13, 21, 22
+    big = block(("fp8",) * 4, "e4m3", B * W, B, W, max_new=N)
+    own = block(("fp8",) * 4, "e4m3", B * W, batch, width, max_new=new)
+    table = dev32(np.arange(batch * width).reshape(batch, width))
+    lens = dev32([max(new, (37 * b) % (width * SIZE)) for b in range(batch)])
+    x = inputs.activations(batch * new, HID, 3).to(dev())
+    assert torch.equal(big.step(x, table, lens), own.step(x, table, lens))
+    big.check()
+    own.check()
+
+
+def test_ragged_step_without_max_new():
+    """off without max_new: any sequence may have as many new tokens as the block allows."""
+    one, two = (block(("fp8",) * 4, "i8", 8, 2, 4, max_new=30) for _ in range(2))
+    table, lens, off = dev32([[0, 1, 2, 3], [4, 5, 6, 7]]), dev32([30, 4]), dev32([0, 30, 32])
+    x = inputs.activations(32, HID, 9).to(dev())
+    assert torch.equal(one.step(x, table, lens, off), two.step(x, table, lens, off, 30))
+    one.check()
+
+
+def test_check_reports_the_shared_quantiser():
+    blk = block(("fp8",) * 4, "i8", 8, 1, 4, max_new=30)
+    x = inputs.activations(30, HID, 9).to(dev())
+    x[3, 7] = float("nan")
+    blk.step(x, dev32([[0, 1, 2, 3]]), dev32([30]))
+    # the append and the last product flag it too: their words are cleared first
+    for ws in (blk._ws_append, blk._ws_fp8, blk._ws_attention):
+        try:
+            hyb.check_status(ws)
+        except hyb.HybError:
+            pass
+    with pytest.raises(hyb.HybError) as ei:
+        blk.check()
+    assert ei.value.flags == hyb.STATUS_NAN
