@@ -434,11 +434,13 @@ HYB_API size_t hyb_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
  * inside the call exactly as hyb_fp8_quant with block_rows 1 would, or e4m3
  * (xdt HYB_E4M3) with its scales xs [m][ceil(k / 128)] (row stride ldxs).  Y is
  * [m][n] (ydt HYB_F32 or HYB_BF16, row stride ldy), written, not accumulated.
+ * k is at most 2^31 - 2049, n 2^31 - 1 and m 2^31 - 1 (8.3 million in the
+ * products of more than 32 tokens).
  * Q and X 16-byte aligned, their row strides multiples of 16 bytes; the last
  * row of each is read up to the next multiple of 16 bytes (what lies there is
  * not used).  A NaN or infinity in a bf16 X sets the status word.  flags: 0 or
- * HYB_LAUNCH_OVERLAP_PREV, with A the weight that the preceding kernel must
- * not write.  The workspace's status word is zeroed before the first call;
+ * HYB_LAUNCH_OVERLAP_PREV, with A the weight that no work queued before the call
+ * and not yet finished may write.  Y must not overlap X.  The workspace's status word is zeroed before the first call;
  * calls of different shapes may share a workspace that is large enough for
  * each.  Results do not depend on the workspace or on earlier calls. */
 HYB_API int hyb_fp8_matmul(const hyb_fp8_matrix *A, int64_t m, const void *X, int64_t ldx,
@@ -511,8 +513,9 @@ HYB_API int hyb_cache_append(const hyb_cache *C, const hyb_sequences *S, const u
                              int64_t ldk, int64_t hsk, const uint16_t *V, int64_t ldv,
                              int64_t hsv, void *ws, size_t ws_bytes, hyb_stream_t stream);
 
-/* Workspace bytes of hyb_cache_attention for these numbers of sequences, new
- * tokens, pages and query heads (with any window); 0 if the arguments are
+/* Workspace bytes of hyb_cache_attention for at most these numbers of sequences,
+ * new tokens and pages, and these query heads (with any window): a workspace
+ * sized for the largest step serves every smaller one.  0 if the arguments are
  * invalid.  The answer depends on the current device (its SM count). */
 HYB_API size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t batch,
                                                    int32_t max_new, int32_t max_pages,
@@ -595,7 +598,9 @@ HYB_API int hyb_spmv_noalloc_check_status(hyb_stream_t stream, uint32_t *flags);
  * data check fired) or HYB_ERR_CUDA. If flags is not NULL it receives the raw
  * status bits (1 = NaN weight seen by hyb_pack, 2 = tile_map byte other than
  * 0/1 or a tile map that does not fit the buffers, 4 = a bounded wait ran
- * out). */
+ * out, 8 = lengths, row offsets or page numbers of hyb_sequences that contradict
+ * one another or the cache; 1 also for a NaN or an infinity that hyb_fp8_quant,
+ * hyb_fp8_matmul or hyb_cache_append saw). */
 HYB_API int hyb_check_status(void *ws, hyb_stream_t stream, uint32_t *flags);
 
 /* Failure-path self test: launch on `stream` a one-CTA kernel whose mbarrier

@@ -271,7 +271,7 @@ int fp8_check(const hyb_fp8_matrix *A) {
   if (!A || !A->q || !A->scale) return HYB_ERR_INVALID_ARG;
   if (A->n < 1 || A->k < 1 || A->ldq < A->k || A->lds < (A->k + kBlk - 1) / kBlk)
     return HYB_ERR_INVALID_ARG;
-  if (A->n > INT32_MAX || A->k > INT32_MAX - kBlk) return HYB_ERR_UNSUPPORTED;
+  if (A->n > INT32_MAX || A->k > kMaxCols) return HYB_ERR_UNSUPPORTED;
   if ((uintptr_t)A->q % 16 != 0 || A->ldq % 16 != 0 || (uintptr_t)A->scale % 4 != 0)
     return HYB_ERR_ALIGNMENT;
   return HYB_OK;
@@ -290,7 +290,7 @@ int hyb_fp8_quant(int64_t rows, int64_t cols, const void *X, int64_t ldx, hyb_dt
   if (!X || !Q || !scale || rows < 1 || cols < 1) return HYB_ERR_INVALID_ARG;
   if (xdt != HYB_F32 && xdt != HYB_BF16) return HYB_ERR_INVALID_ARG;
   if (block_rows != 1 && block_rows != kBlk) return HYB_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || cols > INT32_MAX - kBlk) return HYB_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || cols > kMaxCols) return HYB_ERR_UNSUPPORTED;
   if (ldx < cols || ldq < cols || lds < (cols + kBlk - 1) / kBlk) return HYB_ERR_INVALID_ARG;
   if ((uintptr_t)X % (xdt == HYB_F32 ? 4 : 2) != 0 || (uintptr_t)Q % 16 != 0 || ldq % 16 != 0 ||
       (uintptr_t)scale % 4 != 0)
@@ -303,7 +303,7 @@ int hyb_fp8_quant(int64_t rows, int64_t cols, const void *X, int64_t ldx, hyb_dt
 
 // workspace: header; but for small products also X's scales and values
 size_t hyb_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m < 1 || n < 1 || k < 1 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX - kBlk) return 0;
+  if (m < 1 || n < 1 || k < 1 || m > INT32_MAX || n > INT32_MAX || k > kMaxCols) return 0;
   if (fp8_is_small(m, n, k)) return kHeaderBytes;
   return fp8_x_offset(m, k) + (size_t)m * align_up((size_t)k, 16);
 }

@@ -10,6 +10,9 @@ constexpr int kBlk = 128;  // columns (and rows of W) per scale
 constexpr int kDecodeTokens = 32;
 // The largest weight of the small kernel.
 constexpr int64_t kSmallBytes = 8 << 20;
+// The most columns: those that the kernels count past the last one, a warp's
+// 8 blocks at most, stay within 31 bits.
+constexpr int64_t kMaxCols = INT32_MAX - 16 * kBlk;
 constexpr float kE4m3Max = 448.0f;
 // blocks whose largest value is smaller quantise as if it were this (an all-
 // zero block then needs no case of its own): 448 * 2^-64

@@ -687,6 +687,8 @@ def _scope(index, stream):
     context).  Outputs and workspaces made inside a call are then allocated in
     the order of the stream that uses them."""
     if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"stream of device {stream.device_index}, tensors on device {index}")
         return stream.cuda_stream, torch.cuda.stream(stream)
     if index == torch._C._cuda_getDevice():
         return _raw_stream(index), _NO_SCOPE

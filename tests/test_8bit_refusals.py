@@ -185,3 +185,18 @@ def test_expanded_rows_are_refused():
             hyb.cache_append(C, q[:, :2], q[:, 2:], t, lens)
     with pytest.raises(ValueError, match="CUDA"):
         hyb.cache_attention(C, q[:1], torch.zeros(1, 1, dtype=torch.int32).expand(1, 3).contiguous()[:, :3], lens[:1])
+
+
+def test_largest_sizes(L):
+    """Columns that the quantiser could not count in 31 bits are refused."""
+    big = (1 << 31) - 2048
+    assert quant(L, cols=big, ldx=big, ldq=big, lds=1 << 30) == UNS
+    assert matmul(L, k=big, ldq=big, lds=1 << 30, ldx=big) == UNS
+    assert L.hyb_fp8_workspace_bytes(1, 1, big) == 0 and L.hyb_fp8_workspace_bytes(1, 1, big - 1) > 0
+
+
+def test_stream_of_another_device():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+    with pytest.raises(ValueError, match="device 1"):
+        hyb._scope(0, Stream())
