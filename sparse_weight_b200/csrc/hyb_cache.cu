@@ -778,7 +778,9 @@ void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, i
   const int64_t fit = rows == 8 && units * steps >= 32ll * sms ? 3 : most_per_sm(rows);
   const int64_t fill = fit * sms;
   const bool many = units >= (rows <= 16 ? 8ll * sms : fill) || units > kTickets;
-  const int64_t want = many ? 1 : (fill + units - 1) / units;
+  // (a unit of 256 rows has its SM to itself: a CTA more than there are SMs would
+  // wait for a whole one)
+  const int64_t want = many ? 1 : (rows == kPrefillRows ? fill : fill + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
   if (c < kMinChunk) c = kMinChunk;
   const int64_t top = units >= sms ? kLeastTop : 64;

@@ -13,15 +13,21 @@
 //     V by rows of tokens, read transposed), in a ring of four.
 //   * warp 1 issues S = Q K^T and O += P V with P from tensor memory, for one
 //     tile while the other one's softmax is computed.
-//   * warps 8-11 and 12-15, a row per thread, read S, mask it, take the
-//     maximum, and write P as fp16 over S.  O stays in tensor memory; it is
-//     rescaled only where a row's maximum has grown by more than 2^11 since the
-//     last time (P then stays within fp16).
+//   * warps 8-11 and 12-15, a row per thread, read S half a step at a time (64
+//     values, which stay in registers from S to P), mask it, take the maximum, and
+//     write P as fp16 over S.  O stays in tensor memory; it is rescaled only where
+//     a row's maximum has grown by more than 2^11 since the last time (P then
+//     stays within fp16).
 //
-// Tensor memory: per tile 128 columns of S and D of O.  Bound by the
-// exponentials (16 per clock and SM: 2048 clocks for 256 x 128) and the MMAs at
-// about the same rate.  With steps of 64 tokens the MMAs of N = 64 took longer
-// than the exponentials: they read the 128 rows of Q for half the products.
+// Tensor memory: per tile 128 columns of S and D of O.  A step takes about 5200
+// clocks: 2700 of a tile's softmax, then its two products and their way to the
+// next one, which the other tile's softmax hides in part.  The MMAs alone would
+// take 3100 (96 each, from shared and tensor memory alike), the exponentials 2048.
+// Measured and not kept: P handed over by halves, so that its product starts
+// earlier (118 us instead of 112 at 2 x 1024 tokens over 5120, window 2048: the
+// waits of the MMA warp cost more); S by halves too (129 us: MMAs of N = 64 take as
+// long as those of 128); maxima and exponentials in one pass, repeated where the
+// reference moves (134 us, spills).
 #include "hyb_cache.cuh"
 #include "hyb_tcgen05.cuh"
 
@@ -29,6 +35,7 @@ namespace hyb {
 namespace {
 
 constexpr int kT = kPrefillStep;
+constexpr int kH = kT / 2;  // tokens of a half step
 constexpr int kThreads = 512;
 constexpr int kRaw = 2;  // keys or values of a step on their way
 constexpr int kOps = 4;  // and as fp16 operands
@@ -102,23 +109,20 @@ __device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[32]) {
       : HYB_R32(r)
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 template <int N>
 __device__ __forceinline__ void tmem_got(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));  // not read before the wait
-}
-__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
 }
 #undef HYB_R32
 
@@ -220,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kSc; ++s) mbar_init(&sc_full[s], 1);
     for (int r = 0; r < 2; ++r) {
-      mbar_init(&s_full[r], 1);
-      mbar_init(&p_full[r], 128);
+      mbar_init(&p_full[r], 4);
       mbar_init(&pv_done[r], 1);
+      mbar_init(&s_full[r], 1);
       mbar_init(&o_full[r], 1);
     }
     mbar_init(&q_full, 128 * tiles);
@@ -300,24 +304,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&q_full, 0u) && ready(0);
       for (int r = 0; r < tiles && ok; ++r) scores(0, r);
       for (int j = 0; j < n && ok; ++j) {
+        const uint32_t parity = (uint32_t)j & 1u;
         ok = ready(2 * j + 1);
         for (int r = 0; r < tiles && ok; ++r) {
-          ok = wait(&p_full[r], (uint32_t)j & 1u);
+          const uint64_t v = vd + slot(2 * j + 1);
+          ok = wait(&p_full[r], parity);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v = vd + slot(2 * j + 1);
 #pragma unroll
-          for (int kk = 0; kk < kT / 16; ++kk)
-            umma_ts(leader, tmem + r * Sh::kTile + kT, tmem + r * Sh::kTile + 8 * kk,
-                    v + (kk * 2048 >> 4), (j | kk) != 0, kIdO);
+          for (int kk = 0; kk < kT / 16; ++kk)  // (P of the second half lies 64 columns on)
+            umma_ts(leader, tmem + r * Sh::kTile + kT,
+                    tmem + r * Sh::kTile + (kk >> 2) * kH + 8 * (kk & 3), v + (kk * 2048 >> 4),
+                    (j | kk) != 0, kIdO);
           if (r == tiles - 1) umma_commit_if(leader, &op_empty[(2 * j + 1) % kOps]);
           if (j + 1 == n) {
             umma_commit_if(leader, &o_full[r]);
           } else {
-            // S goes where P lies: its product has to be done (and O may be
-            // rescaled once S is there)
+            // S goes where P lies: its product has to be done
             umma_commit_if(leader, &pv_done[r]);
-            ok = (r > 0 || ready(2 * j + 2)) && wait(&pv_done[r], (uint32_t)j & 1u);
+            ok = (r > 0 || ready(2 * j + 2)) && wait(&pv_done[r], parity);
             if (ok) scores(j + 1, r);
           }
         }
@@ -446,93 +451,119 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the warp's narrowest and widest bounds: outside them a step needs no mask
     const int whi = __reduce_min_sync(0xFFFFFFFFu, live ? bhi : INT32_MAX);
     const int wlo = __reduce_max_sync(0xFFFFFFFFu, live ? blo : 0);
-    for (int j = 0; j < n; ++j) {
-      const int base = base_of(j);
-      ok = ring_wait(&s_full[r], (uint32_t)j & 1u) &&
-           ring_wait(&sc_full[j % kSc], (uint32_t)(j / kSc) & 1u);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const bool edge = base + kT > whi || base < wlo;  // some row of the warp does not see it whole
-      // 32 columns become exponents against the reference: s * scale + log2(vs) - ref
-      auto exponents = [&](int c, uint32_t (&x)[32]) {
+    for (int i2 = 0; i2 < 2 * n; ++i2) {
+      const int j = i2 >> 1, half = i2 & 1, base = base_of(j) + half * kH;
+      if (!half) {
+        ok = ring_wait(&s_full[r], (uint32_t)j & 1u) &&
+             ring_wait(&sc_full[j % kSc], (uint32_t)(j / kSc) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool edge = base + kH > whi || base < wlo;  // some row of the warp does not see it whole
+      const uint32_t th = tl + half * kH;
+      uint32_t x[2][32];
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tmem_get(th, x[0]);
+      tmem_get(th + 32, x[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (c == 0) {
+          tmem_got(x[0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(x[1][e]));
+        }
+        // exponents against the reference: s * scale + log2(vs) - ref
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint64_t f = pair(s_sc[j % kSc][0][2 * c + g] * qm);
-          const uint64_t o = pair(s_sc[j % kSc][1][2 * c + g] - ref);
+          const uint64_t f = pair(s_sc[j % kSc][0][4 * half + 2 * c + g] * qm);
+          const uint64_t o = pair(s_sc[j % kSc][1][4 * half + 2 * c + g] - ref);
 #pragma unroll
-          for (int e = 16 * g; e < 16 * g + 16; e += 2) fma2(x[e], x[e + 1], f, o);
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) fma2(x[c][e], x[c][e + 1], f, o);
         }
         if (edge) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int at = base + 32 * c + e;
-            if (!(at < bhi && (at >= blo || at < p.sinks))) x[e] = 0xFF800000u;  // -infinity
+            if (!(at < bhi && (at >= blo || at < p.sinks))) x[c][e] = 0xFF800000u;  // -infinity
           }
         }
-      };
-      uint32_t x[2][32];  // one half on its way while the other is worked on
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      tmem_get(tl, x[0]);
-#pragma unroll
-      for (int c = 0; c < kT / 32; ++c) {
-        tmem_got(x[c & 1]);
-        tmem_get(tl + 32 * ((c + 1) % (kT / 32)), x[(c + 1) & 1]);  // (at the end the first again)
-        exponents(c, x[c & 1]);
 #pragma unroll
         for (int e = 0; e < 32; e += 8)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            m4[q] = fmaxf(fmaxf(m4[q], __uint_as_float(x[c & 1][e + q])),
-                          __uint_as_float(x[c & 1][e + q + 4]));
+            m4[q] = fmaxf(fmaxf(m4[q], __uint_as_float(x[c][e + q])),
+                          __uint_as_float(x[c][e + q + 4]));
       }
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       const bool need = mx > (fresh_row ? -INFINITY : kLift + kGrow);
       if (__any_sync(0xFFFFFFFFu, need)) {
-        // a new reference: what lies in O and l counts against the old one (the
-        // step before is done: its product was waited for before S was computed)
-        const float by = need ? mx - kLift : 0.0f;
+        // a new reference: what lies in O, l and the first half's P counts against
+        // the old one (a whole number of binades, so that none of it is rounded)
+        const float by = need ? floorf(mx - kLift) : 0.0f;
         ref += by;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) - by);
         if (__any_sync(0xFFFFFFFFu, need && !fresh_row)) {
+          // (the product of the step before is done: it was waited for before S
+          // was computed)
           const float corr = need && !fresh_row ? ex2(-by) : 1.0f;
           l *= corr;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t y[32];
-            tmem_get(tl + kT + 32 * c, y);
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t y[16];
+            tmem_get(tl + kT + 16 * c, y);
             tmem_got(y);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
-            tmem_put(tl + kT + 32 * c, y);
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+            tmem_put(tl + kT + 16 * c, y);
+          }
+          if (half) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t y[16];
+              tmem_get(tl + 16 * c, y);
+              tmem_got(y);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y[e]));
+                const __half2 hp = __floats2half2_rn(f.x * corr, f.y * corr);
+                y[e] = *reinterpret_cast<const uint32_t *>(&hp);
+              }
+              tmem_put(tl + 16 * c, y);
+            }
           }
         }
         fresh_row = fresh_row && !need;
       }
 #pragma unroll
-      for (int c = 0; c < kT / 32; ++c) {
-        tmem_got(x[c & 1]);
-        if (c + 1 < kT / 32) tmem_get(tl + 32 * (c + 1), x[(c + 1) & 1]);
-        exponents(c, x[c & 1]);
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];  // P, pairs of fp16
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint64_t s2 = 0;  // a pair of sums
+          uint64_t s2[2] = {0, 0};  // pairs of sums
 #pragma unroll
           for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-            const float a = ex2(__uint_as_float(x[c & 1][e])), d = ex2(__uint_as_float(x[c & 1][e + 1]));
-            add2(s2, a, d);
+            const float a = ex2(__uint_as_float(x[c][e])), d = ex2(__uint_as_float(x[c][e + 1]));
+            add2(s2[e >> 1 & 1], a, d);
             const __half2 hp = __floats2half2_rn(a, d);
             pk[e / 2] = *reinterpret_cast<const uint32_t *>(&hp);
           }
-          l = fmaf(__uint_as_float((uint32_t)s2) + __uint_as_float((uint32_t)(s2 >> 32)),
-                   s_sc[j % kSc][2][2 * c + g], l);
+          l = fmaf((__uint_as_float((uint32_t)s2[0]) + __uint_as_float((uint32_t)s2[1])) +
+                       (__uint_as_float((uint32_t)(s2[0] >> 32)) + __uint_as_float((uint32_t)(s2[1] >> 32))),
+                   s_sc[j % kSc][2][4 * half + 2 * c + g], l);
         }
-        // over columns of S that have been read (32 c + 31 at least)
-        tmem_put(tl + 16 * c, pk);
+        tmem_put(th + 16 * c, pk);  // over columns of S that have been read
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
-      mbar_arrive(&p_full[r]);
+      __syncwarp();
+      if (half && lane == 0) mbar_arrive(&p_full[r]);
     }
     // O: the last step's product is done
     if (n > 0 && ok) {

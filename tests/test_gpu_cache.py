@@ -431,3 +431,24 @@ def test_attention_workspace_of_the_largest_step():
         a = (C, q[:rows], dev32(table), dev32(lens))
         assert torch.equal(hyb.cache_attention(*a, ws=ws), hyb.cache_attention(*a))
     assert hyb.check_status(ws) == 0
+
+
+@pytest.mark.parametrize("type_", ["e4m3", "i8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_growing_scores(dim, type_):
+    """Scores that grow by many binades along the tokens, within a step and from step to step: what was summed
+    against an earlier, smaller maximum is rescaled."""
+    T, new = 700, 80
+    C, table, off = setup([T], [new], 1, dim, 32, type_, seed=3, poison=False)
+    g = torch.Generator().manual_seed(2)
+    q = queries(new, 4, dim, 1)
+    # all keys along one direction, longer and longer, in ramps of different steepness; queries share its sign
+    u = torch.sign(torch.randn(dim, generator=g))
+    q = (q.abs() * u).to(torch.bfloat16)
+    for page in range(-(-T // 32)):
+        i = int(table[0, page])
+        ramp = (page + torch.arange(32) / 32.0) % 5 / 5 * (127 if type_ == "i8" else 256)
+        C.k[i, 0].copy_((ramp[:, None] * u).to(dev()).to(TYPES[type_]))
+        C.k_scale[i, 0] = 2.0 ** (-9 + page % 3)
+    o, lse = hyb.cache_attention(C, q.to(dev()), dev32(table), dev32([T]), return_lse=True)
+    check_attention(C, table, [T], off, q, o, lse)
