@@ -1,4 +1,5 @@
-"""Build libhyb.so (CUDA, sm_100a) in-tree from sparse_weight_b200/csrc.
+"""Build libhyb.so (CUDA, sm_100a) and its C++ binding _hyb_torch.so in-tree from
+sparse_weight_b200/csrc.
 
     python -m sparse_weight_b200.build [--force]
 
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libhyb.so")
+BINDING = os.path.join(HERE, "_hyb_torch.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -47,8 +49,32 @@ def _compile(src, force):
     return obj
 
 
+def _build_binding(force):
+    """_hyb_torch.so: host code only, against torch's headers and libhyb.so."""
+    src = os.path.join(CSRC, "hyb_torch.cpp")
+    if not force and not _stale(BINDING, [src] + _headers()):
+        return
+    import sysconfig
+
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for inc in (INCLUDE, os.path.join(top, "include"),
+                os.path.join(top, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-I", inc]
+    cmd += [src, "-o", tmp, "-L", HERE, "-l:libhyb.so", "-L", os.path.join(top, "lib"), "-lc10",
+            "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libhyb.so; returns its path."""
+    """Compile every csrc/*.cu for sm_100a, link libhyb.so and build its C++
+    binding; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
@@ -58,6 +84,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [NVCC] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    _build_binding(force)
     if verbose:
         print(LIB)
     return LIB

@@ -5,6 +5,11 @@ memory and the current stream.  Function names follow the C ABI without the
 ``hyb_`` prefix.  bf16 tensors cross as their raw 16-bit patterns.
 
 If ``libhyb.so`` is missing the first call raises; there is no fallback.
+
+The 8-bit operators (quant_fp8, matmul_fp8, cache_append, cache_attention) are
+also bound in C++ (``_hyb_torch.so``), which serves their ordinary calls -- a
+workspace given, the current device and stream -- in a third of the time; other
+calls, and those with an argument at fault, take the Python code below.
 """
 import contextlib
 import ctypes
@@ -711,6 +716,22 @@ def _want(fn, ok, what):
         raise ValueError(f"{fn}: {what}")
 
 
+_native = None
+
+
+def _load_native():
+    """The C++ binding of the 8-bit operators (raises if it has not been built)."""
+    global _native
+    lib()
+    path = os.path.join(_HERE, "_hyb_torch.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"_hyb_torch.so not built ({path}); run "
+                           "`python -m sparse_weight_b200.build`")
+    from . import _hyb_torch
+    _native = _hyb_torch
+    return _native
+
+
 @dataclass(frozen=True)
 class Fp8Matrix:
     """An e4m3 weight with one fp32 scale per 128 x 128 block, on the device."""
@@ -740,6 +761,9 @@ class Fp8Matrix:
             self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
             self.scale.data_ptr(), max(self.scale.stride(0), kb)))
         object.__setattr__(self, "_ref", ctypes.byref(self._struct))
+        object.__setattr__(self, "_at", ctypes.addressof(self._struct))
+        object.__setattr__(self, "_index", self.q.get_device()
+                           if self.q.device == self.scale.device else -1)
 
     def struct(self) -> HybFp8Matrix:
         return self._struct
@@ -757,6 +781,12 @@ def quant_fp8(X: torch.Tensor, block_rows: int = 1, ws: torch.Tensor = None, str
     """hyb_fp8_quant: bf16 or fp32 X [rows][cols] -> (q float8_e4m3fn [rows][cols],
     scale fp32 [ceil(rows / block_rows)][ceil(cols / 128)]).  The rows of q lie a
     multiple of 16 bytes apart, as the products need them."""
+    if ws is not None and stream is None:
+        r = (_native or _load_native()).quant_fp8(X, block_rows, ws)
+        if r is not None:
+            if type(r) is int:
+                raise HybError("hyb_fp8_quant", r)
+            return r
     f = "quant_fp8"
     xdt = _QUANT_TYPES.get(X.dtype)
     if xdt is None or X.dim() != 2:
@@ -821,6 +851,12 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
     """hyb_fp8_matmul: Y[m][n] = W X for an e4m3 weight and any number of tokens.
     X is bf16 [m][k] (or [k]), quantised inside the call, or float8_e4m3fn with
     its scales xs (quant_fp8).  flags as for spmm_skinny."""
+    if ws is not None and stream is None:
+        r = (_native or _load_native()).matmul_fp8(A._at, A._index, X, xs, Y, ydt, flags, ws)
+        if r is not None:
+            if type(r) is int:
+                raise HybError("hyb_fp8_matmul", r)
+            return r
     f = "matmul_fp8"
     if X.dim() == 1:
         X = X.view(1, -1)
@@ -903,6 +939,8 @@ class Cache:
             self.v_scale.data_ptr(), HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages,
             heads, size, dim, sp, sh, st))
         object.__setattr__(self, "_ref", ctypes.byref(self._struct))
+        object.__setattr__(self, "_at", ctypes.addressof(self._struct))
+        object.__setattr__(self, "_index", self.k.get_device())
 
     @property
     def page_size(self) -> int:
@@ -971,6 +1009,13 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
     """hyb_cache_append: store new keys and values (bf16 [rows][kv_heads][head_dim])
     as the last tokens of sequences whose lengths are ``lens`` with them.  off
     [batch + 1]: the sequences' rows (None: max_new rows each)."""
+    if ws is not None and stream is None:
+        r = (_native or _load_native()).cache_append(C._at, C._index, K, V, page_table, lens, off,
+                                                     max_new, ws)
+        if r is not None:
+            if type(r) is int:
+                raise HybError("hyb_cache_append", r)
+            return
     f = "cache_append"
     c = C._struct
     heads, dim = c.kv_heads, c.head_dim
@@ -1013,6 +1058,14 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     visible (sinks) where window > 0.  scale defaults to 1 / sqrt(head_dim).
     Returns O (bf16, as Q), with return_lse also the fp32 log-sum-exp
     [rows][heads]."""
+    if ws is not None and stream is None:
+        r = (_native or _load_native()).cache_attention(C._at, C._index, Q, page_table, lens, off,
+                                                        max_new, scale, window, sinks, out,
+                                                        return_lse, ws)
+        if r is not None:
+            if type(r) is int:
+                raise HybError("hyb_cache_attention", r)
+            return r
     f = "cache_attention"
     c = C._struct
     dim = c.head_dim

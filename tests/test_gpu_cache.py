@@ -452,3 +452,44 @@ def test_attention_growing_scores(dim, type_):
         C.k_scale[i, 0] = 2.0 ** (-9 + page % 3)
     o, lse = hyb.cache_attention(C, q.to(dev()), dev32(table), dev32([T]), return_lse=True)
     check_attention(C, table, [T], off, q, o, lse)
+
+
+def test_both_bindings_agree():
+    """The C++ binding and the Python code (which a given stream takes) make the same calls, errors among them."""
+    from sparse_weight_b200.hyb import _load_native
+    nat = _load_native()
+    here = torch.cuda.current_stream()
+    lens, new = [90, 33, 0], [4, 2, 1]
+    C, table, off = setup(lens, new, 2, 64, 16, "i8", seed=1, poison=False)
+    D, _, _ = setup(lens, new, 2, 64, 16, "i8", seed=1, poison=False)
+    q, t, n, o = queries(7, 8, 64, 1).to(dev()), dev32(table), dev32(lens), dev32(off)
+    kv = queries(7, 4, 64, 2).to(dev())
+    ws = hyb.new_workspace(hyb.cache_attention_workspace_bytes(C, 3, 8, 4, table.shape[1] * 16), dev())
+    for X, st in ((C, None), (D, here)):
+        hyb.cache_append(X, kv[:, :2], kv[:, 2:], t, n, o, 4, ws=ws, stream=st)
+    for w in ("k", "v", "k_scale", "v_scale"):
+        assert torch.equal(getattr(C, w), getattr(D, w)), w
+    for kw in ({}, dict(window=9, sinks=2), dict(scale=0.3), dict(return_lse=True)):
+        for a in ((C, q, t, n, o, 4), (C, q[:3], t, n), (C, q[:1], t[:1], n[:1]), (C, q[:, ::2], t, n, o, 4)):
+            u, v = hyb.cache_attention(*a, ws=ws, **kw), hyb.cache_attention(*a, ws=ws, stream=here, **kw)
+            u, v = (u, v) if kw.get("return_lse") else ((u,), (v,))
+            for x, y in zip(u, v):
+                assert x.shape == y.shape and x.stride() == y.stride() and torch.equal(x, y)
+    out = torch.zeros(7, 9, 72, dtype=torch.bfloat16, device=dev())[:, :8, :64]
+    assert hyb.cache_attention(C, q, t, n, o, 4, out=out, ws=ws) is out
+    assert torch.equal(out, hyb.cache_attention(C, q, t, n, o, 4))
+    at = (C._at, C._index)
+    for args in ((*at, q.float(), t, n, o, 4), (*at, q, t.long(), n, o, 4), (*at, q, t, n[:2], o, 4), (*at, q, t, n, o, None),
+                 (*at, q, t[:1].expand(3, table.shape[1]), n, o, 4), (*at, q, t, n, None, 4), (*at, q.cpu(), t, n, o, 4),
+                 (*at, q[:, :, :32], t, n, o, 4), (C._at, -1, q, t, n, o, 4)):
+        assert nat.cache_attention(*args, None, 0, 0, None, False, ws) is None
+    assert nat.cache_attention(*at, q, t, n, o, 4, None, 0, 0, out[:, :7], False, ws) is None
+    assert nat.cache_append(*at, kv[:, :2], kv[:6, 2:], t, n, o, 4, ws) is None
+    assert nat.cache_append(*at, kv[:, :3], kv[:, :3], t, n, o, 4, ws) is None
+    for st in (None, here):
+        with pytest.raises(hyb.HybError) as ei:
+            hyb.cache_attention(C, q[:, :7], t, n, o, 4, ws=ws, stream=st)
+        assert ei.value.status == hyb.HYB_ERR_INVALID_ARG
+        with pytest.raises(hyb.HybError) as ei:
+            hyb.cache_append(C, kv[:, :2], kv[:, 2:], t, n, o, 4, ws=ws[:100], stream=st)
+        assert ei.value.status == hyb.HYB_ERR_WORKSPACE

@@ -177,3 +177,48 @@ def test_matmul_streams_graphs_and_shared_workspace():
         f2 = hyb.matmul_fp8(A, xa, ws=ws, flags=hyb.LAUNCH_OVERLAP_PREV)
         assert torch.equal(f, ya) and torch.equal(f2, ya)
     assert hyb.check_status(ws) == 0
+
+
+def test_both_bindings_agree():
+    """The C++ binding and the Python code (which a given stream takes) make the same calls, errors among them."""
+    from sparse_weight_b200.hyb import _load_native
+    nat = _load_native()
+    here = torch.cuda.current_stream()
+    x = values(20, 300, 1)
+    ws = hyb.new_workspace(hyb.fp8_workspace_bytes(20, 130, 300), dev())
+    for X in (x, x.float(), x[:1], x[::2], x[:, 8:40], x.t()[:1]):
+        X = X.to(dev())
+        for block_rows in (1, 128):
+            a, b = hyb.quant_fp8(X, block_rows, ws), hyb.quant_fp8(X, block_rows, ws, stream=here)
+            for u, v in zip(a, b):
+                assert u.shape == v.shape and u.stride() == v.stride() and u.dtype == v.dtype
+                assert torch.equal(u.view(torch.uint8), v.view(torch.uint8))
+    A = hyb.pack_fp8(values(130, 300, 2).to(dev()))
+    pad = torch.zeros(20, 304, dtype=torch.bfloat16, device=dev())
+    pad[:, :300] = x.to(dev())
+    X = pad[:, :300]
+    xq, xs = hyb.quant_fp8(X, 1, ws)
+    for ydt, yt in ((hyb.HYB_F32, torch.float32), (hyb.HYB_BF16, torch.bfloat16)):
+        for u, s in ((X, None), (X[:1], None), (xq, xs), (xq[:7], xs[:7]), (xq[::3], xs[::3])):
+            a = hyb.matmul_fp8(A, u, s, ydt=ydt, ws=ws)
+            assert a.dtype == yt and torch.equal(a, hyb.matmul_fp8(A, u, s, ydt=ydt, ws=ws, stream=here))
+            Y = torch.zeros(u.shape[0], 140, dtype=yt, device=dev())
+            assert hyb.matmul_fp8(A, u, s, Y=Y[:, 3:133], ydt=ydt, ws=ws).data_ptr() == Y[:, 3:133].data_ptr()
+            assert torch.equal(Y[:, 3:133], a)
+    # what the C++ binding does not serve it leaves alone
+    bf = torch.bfloat16
+    for args in ((A._at, A._index, X.float(), None, None, 0, 0, ws), (A._at, A._index, X.cpu(), None, None, 0, 0, ws),
+                 (A._at, A._index, X, None, None, 2, 0, ws), (A._at, A._index, X, None, None, 0, -1, ws),
+                 (A._at, A._index, X[0], None, None, 0, 0, ws), (A._at, A._index, xq, None, None, 0, 0, ws),
+                 (A._at, A._index, X, None, Y.to(bf), 0, 0, ws), (A._at, -1, X, None, None, 0, 0, ws),
+                 (A._at, A._index, xq, xs[:1].expand(20, 3), None, 0, 0, ws)):
+        assert nat.matmul_fp8(*args) is None
+    for args in ((X.half(), 1, ws), (X, 2, ws), (X[:1].expand(4, 300), 1, ws), (X[0], 1, ws), (X.t(), 1, ws), (X, 1, None)):
+        assert nat.quant_fp8(*args) is None
+    with pytest.raises(hyb.HybError) as one:
+        hyb.matmul_fp8(A, X, flags=6, ws=ws)
+    with pytest.raises(hyb.HybError) as two:
+        hyb.matmul_fp8(A, X, flags=6, ws=ws, stream=here)
+    assert str(one.value) == str(two.value) and one.value.status == two.value.status
+    with pytest.raises(hyb.HybError):
+        hyb.quant_fp8(X, 1, ws[:100])
