@@ -176,9 +176,11 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
 
 constexpr int kStep = 32;   // tokens per step
 constexpr int kWarps = 4;   // warps that compute
-// probabilities are held times 2^15 (exp2 of t - max + 15): fp16's 11 bits then
-// reach down to 2^-29 of the largest one and its steps to 2^-39
-constexpr float kLift = 15.0f;
+// Probabilities are held times 2^4 where the reference of the exponentials is the
+// largest exponent, and times 2^15 at most: the reference moves only where it has
+// been outgrown by more (a vote instead of a maximum over lanes in most steps).
+// fp16's smallest step is then at most 2^-28 of the largest probability.
+constexpr float kLift = 4.0f, kGrow = 11.0f;
 
 // D += A B, fp16 operands, fp32 accumulation
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -366,13 +368,15 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   }
 
   float o[MT][NR][4];
-  float m[NR][2], l[NR][2];
+  float m[NR][2], l[NR][2];  // of a row: the reference, and the sum of P / vs
   if (computes) {
-    auto load_scales = [&](int id, float &ks, float &vs) { page_scales(p, id, h, ks, vs); };
+    // (lane l also holds the scales of its page: K's, and V's logarithm and reciprocal)
     int id_cur = load_ids(0), id_nxt = load_ids(16);
-    float ks_cur, vs_cur, ks_nxt, vs_nxt;
-    load_scales(id_cur, ks_cur, vs_cur);
-    load_scales(id_nxt, ks_nxt, vs_nxt);
+    float ks_cur, vs_cur, ks_nxt, vs_nxt, lv_cur, iv_cur;
+    page_scales(p, id_cur, h, ks_cur, vs_cur);
+    page_scales(p, id_nxt, h, ks_nxt, vs_nxt);
+    lv_cur = __log2f(vs_cur);
+    iv_cur = __fdividef(1.0f, vs_cur);
     if constexpr (!SHARE) {
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
@@ -439,16 +443,18 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
       if ((j & 15) == 0 && j) {
         id_cur = id_nxt;
         ks_cur = ks_nxt;
-        vs_cur = vs_nxt;
+        lv_cur = __log2f(vs_nxt);
+        iv_cur = __fdividef(1.0f, vs_nxt);
         id_nxt = load_ids(j + 16);
-        load_scales(id_nxt, ks_nxt, vs_nxt);
+        page_scales(p, id_nxt, h, ks_nxt, vs_nxt);
       }
       const int src = 2 * (j & 15);
-      float ks[2], vs[2];
+      float ks[2], lv[2], iv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         ks[i] = __shfl_sync(0xFFFFFFFFu, ks_cur, src + i);
-        vs[i] = __shfl_sync(0xFFFFFFFFu, vs_cur, src + i);
+        lv[i] = __shfl_sync(0xFFFFFFFFu, lv_cur, src + i);
+        iv[i] = __shfl_sync(0xFFFFFFFFu, iv_cur, src + i);
       }
       const int slot = j % NS;
       const uint32_t kb = ring32 + slot * (2 * kBox), vb = kb + kBox;
@@ -486,17 +492,9 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
         }
 
         // t = s + log2(vs): P then carries the page's value scale, and the
-        // running maximum keeps it within fp16
+        // reference keeps it within fp16
         const bool edge = base + kStep > hi_min || base < lo_max;  // some row does not see it whole
         uint32_t pf[2][NR][2];
-        float corr[NR][2];
-        bool moved = false;
-        float lv[2], iv[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          lv[i] = __log2f(vs[i]);
-          iv[i] = __fdividef(1.0f, vs[i]);
-        }
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -517,37 +515,31 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
               }
           asm volatile("" ::: "memory");
         }
+        float top[NR][2];
+        bool need = false;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
+        for (int n = 0; n < NR; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float v = fmaxf(fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c])), m[n][c]);
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-            const float safe = v == -INFINITY ? 0.0f : v;
-            corr[n][c] = ex2(m[n][c] - safe);
-            moved |= corr[n][c] != 1.0f;
-            m[n][c] = v;
-            const float ref = safe - kLift;
-            float sum[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              s[i][n][c] = ex2(s[i][n][c] - ref);
-              s[i][n][2 + c] = ex2(s[i][n][2 + c] - ref);
-              sum[i] = s[i][n][c] + s[i][n][2 + c];
-            }
-            l[n][c] = fmaf(l[n][c], corr[n][c], fmaf(sum[0], iv[0], sum[1] * iv[1]));
+            top[n][c] = fmaxf(fmaxf(s[0][n][c], s[0][n][2 + c]), fmaxf(s[1][n][c], s[1][n][2 + c]));
+            need |= top[n][c] > m[n][c] + kGrow;
           }
+        if (__any_sync(0xFFFFFFFFu, need)) {
+          // the largest exponents become the references; what is summed counts
+          // against the old ones
+          float corr[NR][2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              const __half2 hp = __floats2half2_rn(s[i][n][2 * d], s[i][n][2 * d + 1]);
-              pf[i][n][d] = movmatrix(*reinterpret_cast<const uint32_t *>(&hp));
+            for (int c = 0; c < 2; ++c) {
+              float v = fmaxf(top[n][c], m[n][c]);
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+              corr[n][c] = ex2(m[n][c] - (v == -INFINITY ? 0.0f : v));
+              m[n][c] = v;
+              l[n][c] *= corr[n][c];
             }
-        }
-        if (__any_sync(0xFFFFFFFFu, moved)) {
 #pragma unroll
           for (int k = 0; k < MT; ++k)
 #pragma unroll
@@ -556,6 +548,29 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
               o[k][n][1] *= corr[n][1];
               o[k][n][2] *= corr[n][0];
               o[k][n][3] *= corr[n][1];
+            }
+          asm volatile("" ::: "memory");  // (a branch of its own: few steps take it)
+        }
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float ref = (m[n][c] == -INFINITY ? 0.0f : m[n][c]) - kLift;
+            float sum[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              s[i][n][c] = ex2(s[i][n][c] - ref);
+              s[i][n][2 + c] = ex2(s[i][n][2 + c] - ref);
+              sum[i] = s[i][n][c] + s[i][n][2 + c];
+            }
+            l[n][c] += fmaf(sum[0], iv[0], sum[1] * iv[1]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const __half2 hp = __floats2half2_rn(s[i][n][2 * d], s[i][n][2 * d + 1]);
+              pf[i][n][d] = movmatrix(*reinterpret_cast<const uint32_t *>(&hp));
             }
         }
 
