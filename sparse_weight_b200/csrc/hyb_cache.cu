@@ -774,14 +774,15 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
 
 // The split of a unit's steps over CTAs: as many CTAs as fit the GPU at a time
 // (3 per SM for units of 8 rows, 2 for 16 and 64, 1 for 256; a third more where
-// all the work is small and the CTAs' start counts), none below 4 steps.  Where
+// all the work is small and the CTAs' start counts), none below 4 steps; units of 8
+// or 16 rows and up to 12 steps are left whole.  Where
 // units alone fill the GPU, and there for units of few rows only, a CTA has at
 // most 40 steps (else 64), so that sequences of different lengths end at about
 // the same time: 32 sequences of 1024 to 8192 tokens took 49.6 us with 48 steps
 // and 46.9 us with 32, one of 65536 45 us with 32 and 36 us with 40.  Only units
 // that are split have tickets, which lie at a fixed place whatever the call's
 // shape, so that calls of different shapes can share a workspace.
-constexpr int kMinChunk = 4;
+constexpr int kMinChunk = 4, kUnsplit = 12;
 constexpr int kShareRows = 64;  // most rows of mma.sync units
 constexpr int kTickets = 2048;
 constexpr int kLeastTop = 40;
@@ -797,7 +798,9 @@ void split_plan(int64_t units, int rows, int64_t tokens, int sms, int *splits, i
   // wait for a whole one)
   const int64_t want = many ? 1 : (rows == kPrefillRows ? fill : fill + units - 1) / units;
   int64_t c = (steps + want - 1) / want;
-  if (c < kMinChunk) c = kMinChunk;
+  // (one short sequence of 300 tokens: 6.2 us in one part per unit, 7.8 in three)
+  const int64_t least = rows <= 16 && steps <= kUnsplit ? kUnsplit : kMinChunk;
+  if (c < least) c = least;
   const int64_t top = units >= sms ? kLeastTop : 64;
   if (c > top && !many && rows <= 16) c = top;
   const int64_t most = kMergeRows / rows;  // parts that the last CTA can add

@@ -21,6 +21,7 @@ namespace hyb {
 namespace {
 
 constexpr int kWarps = 4, kRows = 16, kToks = 8;
+constexpr int kMaxC = 8;  // CTAs of a cluster at most
 
 // D += A B, one m16n8k32 e4m3 product with fp32 accumulation
 __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -155,15 +156,26 @@ __global__ void __launch_bounds__(32 * kWarps) fp8_small_kernel(const Fp8Params 
   for (int c = 0; c < 4; ++c) part[warp][2 * t + (c & 1)][8 * (c >> 1) + g] = acc[c];
   __syncthreads();
   if (C > 1) cluster.sync();
-  // 128 sums, one per thread of the cluster's CTAs in turn
-  for (int e = rank + C * (int)threadIdx.x; e < kRows * kToks; e += C * 32 * kWarps) {
+  // 128 sums at most, a stretch of them per CTA, one per thread; all parts on
+  // their way at once, then added in order
+  const int sums = kRows * (int)p.m, share = (sums + C - 1) / C;
+  const int e = rank * share + (int)threadIdx.x;
+  if ((int)threadIdx.x < share && e < sums) {
     const int row = e % kRows, tok = e / kRows;
-    float s = 0.0f;
-    for (int j = 0; j < C; ++j)
+    float a[kMaxC][kWarps];
 #pragma unroll
-      for (int q = 0; q < kWarps; ++q)
-        s += C == 1 ? part[q][tok][row] : *cluster.map_shared_rank(&part[q][tok][row], j);
-    if (tok < p.m && row0 + row < p.n) {
+    for (int j = 0; j < kMaxC; ++j)
+      if (j < C)
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q)
+          a[j][q] = C == 1 ? part[q][tok][row] : *cluster.map_shared_rank(&part[q][tok][row], j);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMaxC; ++j)
+      if (j < C)
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) s += a[j][q];
+    if (row0 + row < p.n) {
       const int64_t at = tok * p.ldy + row0 + row;
       if (p.bf16_out)
         static_cast<uint16_t *>(p.Y)[at] = f32_to_bf16_rne(s);
@@ -183,13 +195,13 @@ int launch_small(const Fp8Params &p, int C, cudaStream_t st) {
 }  // namespace
 
 bool fp8_is_small(int64_t m, int64_t n, int64_t k) {
-  return m <= kToks && k <= 8 * kWarps * 4 * kBlk && n * k <= kSmallBytes;
+  return m <= kToks && k <= kMaxC * kWarps * 4 * kBlk && n * k <= kSmallBytes;
 }
 
 int fp8_small(const Fp8Params &p, cudaStream_t st) {
   const int64_t kb = (p.k + kBlk - 1) / kBlk;
   // two blocks per warp where a cluster of 8 covers k with them, else four
-  const int u = kb <= 8 * kWarps * 2 ? 2 : 4;
+  const int u = kb <= kMaxC * kWarps * 2 ? 2 : 4;
   const int C = (int)((kb + u * kWarps - 1) / (u * kWarps));
   if (u == 2)
     return p.x_bf16 ? launch_small<2, true>(p, C, st)
