@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   __shared__ float s_m[kWarps][8 * NR], s_l[kWarps][8 * NR];
   __shared__ uint32_t s_last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) prefetch_maps(kmap, vmap);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -371,12 +372,10 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
   float m[NR][2], l[NR][2];  // of a row: the reference, and the sum of P / vs
   if (computes) {
     // (lane l also holds the scales of its page: K's, and V's logarithm and reciprocal)
-    int id_cur = load_ids(0), id_nxt = load_ids(16);
+    // (the first bytes set out as soon as their pages are known, what the steps
+    // behind them need only after that)
+    int id_cur = load_ids(0), id_nxt;
     float ks_cur, vs_cur, ks_nxt, vs_nxt, lv_cur, iv_cur;
-    page_scales(p, id_cur, h, ks_cur, vs_cur);
-    page_scales(p, id_nxt, h, ks_nxt, vs_nxt);
-    lv_cur = __log2f(vs_cur);
-    iv_cur = __fdividef(1.0f, vs_cur);
     if constexpr (!SHARE) {
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
@@ -385,6 +384,7 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
         if (j < mine && lane == 0) issue(j, a, c);
       }
     }
+    page_scales(p, id_cur, h, ks_cur, vs_cur);
 
     // Q: row g of each tile, times a power of two that brings its largest value
     // to [128, 256), so that bf16's 8 bits survive the change to fp16
@@ -438,6 +438,11 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
       for (int n = 0; n < NR; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[k][n][c] = 0.0f;
+
+    lv_cur = __log2f(vs_cur);
+    iv_cur = __fdividef(1.0f, vs_cur);
+    id_nxt = load_ids(16);
+    page_scales(p, id_nxt, h, ks_nxt, vs_nxt);
 
     for (int j = 0; j < mine; ++j) {
       if ((j & 15) == 0 && j) {
@@ -709,16 +714,7 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
     }
   }
   if (alone) return;
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t n = atomicAdd(p.tickets + unit, 1u);
-    s_last = n == (uint32_t)active - 1u;
-    if (s_last) p.tickets[unit] = 0;  // ready for the next call
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
+  if (!last_of_unit(p, unit, active, &s_last)) return;
   merge_parts<D, Sh::kRows, Sh::kThreads>(p, p.part + (int64_t)unit * p.splits * Sh::kPart, active,
                                           urows, u0, row0, h, kLift,
                                           reinterpret_cast<float *>(smem));

@@ -92,6 +92,29 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+// (kernel parameters: open before the preceding kernel has ended)
+__device__ __forceinline__ void prefetch_maps(const CUtensorMap &a, const CUtensorMap &b) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a)) : "memory");
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&b)) : "memory");
+}
+
+// Whether this CTA is the last of its unit's `active` ones; the parts of all are
+// then visible to its threads (read past L1).  One thread's fences between two
+// barriers order the whole CTA's writes and reads.
+__device__ __forceinline__ bool last_of_unit(const AttnParams &p, int unit, int active,
+                                             uint32_t *s_last) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const uint32_t n = atomicAdd(p.tickets + unit, 1u);
+    *s_last = n == (uint32_t)active - 1u;
+    if (*s_last) p.tickets[unit] = 0;  // ready for the next call
+    __threadfence();
+  }
+  __syncthreads();
+  return *s_last != 0;
+}
+
 // two 8-bit values (the low or high half of w) as a pair of fp16, exactly
 template <bool I8, int HALF>
 __device__ __forceinline__ uint32_t to_f16x2(uint32_t w) {

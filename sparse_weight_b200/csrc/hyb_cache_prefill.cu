@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_sc[kSc][3][kT / 16];  // scale of K, log2 of V's, its reciprocal, per 16 tokens
   __shared__ uint32_t s_tmem, s_last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) prefetch_maps(kmap, vmap);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = (int)(blockIdx.x % (unsigned)p.splits);
@@ -627,16 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (active == 1) return;
 
   // the unit's last CTA adds the parts in order
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t at = atomicAdd(p.tickets + unit, 1u);
-    s_last = at == (uint32_t)active - 1u;
-    if (s_last) p.tickets[unit] = 0;  // ready for the next call
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
+  if (!last_of_unit(p, unit, active, &s_last)) return;
   merge_parts<D, kPrefillRows, kThreads>(p, p.part + (int64_t)unit * p.splits * Sh::kPart, active,
                                          urows, u0, row0, h, 0.0f, reinterpret_cast<float *>(smem));
 }
