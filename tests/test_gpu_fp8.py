@@ -222,3 +222,19 @@ def test_both_bindings_agree():
     assert str(one.value) == str(two.value) and one.value.status == two.value.status
     with pytest.raises(hyb.HybError):
         hyb.quant_fp8(X, 1, ws[:100])
+
+
+@pytest.mark.parametrize("ydt", [hyb.HYB_F32, hyb.HYB_BF16])
+@pytest.mark.parametrize("m,n,k", [(257, 12900, 300), (500, 9400, 260), (640, 12992, 128), (385, 14336, 513)])
+def test_matmul_wide(m, n, k, ydt):
+    """Products whose tiles fill the GPU: CTAs of 256 columns, two blocks of W's scales each."""
+    A, wq, ws = weight(n, k, m + n + k)
+    x = values(m, -(-k // 8) * 8, 7 * m + k)[:, :k]
+    xd = torch.zeros(m, -(-k // 8) * 8, dtype=torch.bfloat16, device=dev())[:, :k]
+    xd.copy_(x)
+    w = hyb.new_workspace(hyb.fp8_workspace_bytes(m, n, k), dev())
+    Y = torch.full((m + 1, n + 8), 3.0, dtype=torch.float32 if ydt == hyb.HYB_F32 else torch.bfloat16, device=dev())
+    hyb.matmul_fp8(A, xd, Y=Y[:m, :n], ydt=ydt, ws=w)
+    assert hyb.check_status(w) == 0
+    assert (Y[m] == 3).all() and (Y[:, n:] == 3).all()
+    check(Y[:m, :n], x, wq, ws, k)
