@@ -56,6 +56,8 @@ struct PShape {
   static_assert(2 * kTile <= 512, "tensor memory");
 };
 constexpr int kTmem = 512;
+// (With its 512 threads of 121 to 128 registers a CTA has its SM to itself: none of
+// a kernel that starts early, with tensor memory of its own, can be beside it.)
 
 // The MMA warp runs as a whole and only its leader's instructions take effect:
 // operands then stay in uniform registers (from a branch of one lane they were
