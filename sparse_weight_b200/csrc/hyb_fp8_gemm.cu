@@ -20,8 +20,9 @@
 //     partial sums meet in distributed shared memory in a fixed order.
 //
 // Bound by the epilogue's reads of tensor memory and FMAs beside the MMAs.  2048
-// tokens x 14336 x 4096: 170 us (1.41 PFLOP/s) with BN = 256, the quantiser
-// included (BN = 224, whose 6.9 rounds of CTAs waste less than 6.05: 176 us); 45 x
+// tokens x 14336 x 4096: 168 us (1.43 PFLOP/s) with BN = 256, the quantiser
+// included (BN = 224, whose 6.9 rounds of CTAs waste less than 6.05, 176 us; rows of W
+// first, 171 us, W read three times); 45 x
 // 1000 x 4100 in e4m3: 7.7 us, latency.
 #include "hyb_fp8.cuh"
 #include "hyb_tcgen05.cuh"
@@ -35,6 +36,7 @@ namespace {
 
 constexpr int kTok = 128;       // tokens per CTA
 constexpr int kMaxC = 8;        // CTAs of a cluster at most
+constexpr int kGroup = 16;      // token tiles that pass along W together
 
 template <int BN>
 struct Shape {
@@ -157,7 +159,16 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads)
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t n0 = (int64_t)(blockIdx.x / C) * BN, m0 = (int64_t)blockIdx.y * kTok;
+  // the tile: token tiles first, kGroup of them at a time, then along W, so that a
+  // group's X stays in L2 while W passes once
+  int64_t n0, m0;
+  {
+    const int64_t wt = gridDim.x / C, t = (int64_t)blockIdx.y * wt + blockIdx.x / C;
+    const int64_t first = t / (kGroup * wt) * kGroup, in = t - first * wt;
+    const int64_t toks = min((int64_t)kGroup, (int64_t)gridDim.y - first);
+    m0 = (first + in % toks) * kTok;
+    n0 = in / toks * BN;
+  }
   const int kb = (int)((p.k + kBlk - 1) / kBlk);
   const int b0 = (int)((int64_t)kb * rank / C), nb = (int)((int64_t)kb * (rank + 1) / C) - b0;
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);

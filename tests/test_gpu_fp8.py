@@ -225,7 +225,8 @@ def test_both_bindings_agree():
 
 
 @pytest.mark.parametrize("ydt", [hyb.HYB_F32, hyb.HYB_BF16])
-@pytest.mark.parametrize("m,n,k", [(257, 12900, 300), (500, 9400, 260), (640, 12992, 128), (385, 14336, 513)])
+@pytest.mark.parametrize("m,n,k", [(257, 12900, 300), (500, 9400, 260), (640, 12992, 128), (385, 14336, 513),
+                                   (2200, 2560, 130)])
 def test_matmul_wide(m, n, k, ydt):
     """Products whose tiles fill the GPU: CTAs of 256 columns, two blocks of W's scales each."""
     A, wq, ws = weight(n, k, m + n + k)
