@@ -22,8 +22,9 @@
 // Bound by the epilogue's reads of tensor memory and FMAs beside the MMAs.  2048
 // tokens x 14336 x 4096: 168 us (1.43 PFLOP/s) with BN = 256, the quantiser
 // included (BN = 224, whose 6.9 rounds of CTAs waste less than 6.05, 176 us; rows of W
-// first, 171 us, W read three times); 45 x
-// 1000 x 4100 in e4m3: 7.7 us, latency.
+// first, 171 us, W read three times); 45 x 1000 x 4100 in e4m3: 6.9 us, latency;
+// 128 x 4096 x 4096 in bf16: 15 us, and 33 us when the lanes that add up a cluster's
+// sums read 32 bytes apart from one another.
 #include "hyb_fp8.cuh"
 #include "hyb_tcgen05.cuh"
 
@@ -281,57 +282,56 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads)
   __syncthreads();  // warps that wait here do not poll, as they would in the cluster's barrier
   if (C > 1) cluster.sync();
 
-  // the cluster's CTAs share the rows: a warp takes a row of BN sums at a time
+  // the cluster's CTAs share the rows: a warp takes a row of BN sums at a time, four
+  // neighbours per lane
   {
     const int rows = (int)min((int64_t)kTok, p.m - m0);
     const float *mine = reinterpret_cast<const float *>(smem);
     const int es = p.bf16_out ? 2 : 4;
-    const bool vec = ((uintptr_t)p.Y % 16 == 0) && (p.ldy * es % 16 == 0);
+    const bool vec = ((uintptr_t)p.Y % (4 * es) == 0) && (p.ldy % 4 == 0);
     for (int r = rank + C * warp; r < rows; r += C * (Sh::kThreads / 32)) {
-      for (int c = lane * 8; c < BN; c += 256) {
-        constexpr int kParts = BN == 256 ? 1 : kMaxC;  // (the wide shape is not clustered)
-        float4 a[kParts][2];  // all on their way at once, then added in order
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          if (q < C) {
-            const float *src = C == 1 ? mine : cluster.map_shared_rank(mine, q);
-            a[q][0] = *reinterpret_cast<const float4 *>(src + r * Sh::kPitch + c);
-            a[q][1] = *reinterpret_cast<const float4 *>(src + r * Sh::kPitch + c + 4);
-          }
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int c = lane * 4; c < BN; c += 128) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (C == 1) {
+          v = *reinterpret_cast<const float4 *>(mine + r * Sh::kPitch + c);
+        } else {
+          float4 a[kMaxC];  // all on their way at once, then added in order
 #pragma unroll
-        for (int q = 0; q < kParts; ++q)
-          if (q < C)
+          for (int q = 0; q < kMaxC; ++q)
+            if (q < C)
+              a[q] = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(mine, q) +
+                                                       r * Sh::kPitch + c);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              v[4 * h] += a[q][h].x;
-              v[4 * h + 1] += a[q][h].y;
-              v[4 * h + 2] += a[q][h].z;
-              v[4 * h + 3] += a[q][h].w;
+          for (int q = 0; q < kMaxC; ++q)
+            if (q < C) {
+              v.x += a[q].x;
+              v.y += a[q].y;
+              v.z += a[q].z;
+              v.w += a[q].w;
             }
+        }
         const int64_t n = n0 + c, at = (m0 + r) * p.ldy + n;
+        const float o[4] = {v.x, v.y, v.z, v.w};
         if (p.bf16_out) {
           uint16_t *y = static_cast<uint16_t *>(p.Y) + at;
-          if (vec && n + 8 <= p.n) {
-            uint32_t w[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = f32_to_bf16_rne(v[2 * q]) | ((uint32_t)f32_to_bf16_rne(v[2 * q + 1]) << 16);
-            *reinterpret_cast<uint4 *>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (vec && n + 4 <= p.n) {
+            *reinterpret_cast<uint2 *>(y) =
+                make_uint2(f32_to_bf16_rne(o[0]) | ((uint32_t)f32_to_bf16_rne(o[1]) << 16),
+                           f32_to_bf16_rne(o[2]) | ((uint32_t)f32_to_bf16_rne(o[3]) << 16));
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (n + q < p.n) y[q] = f32_to_bf16_rne(v[q]);
+            for (int q = 0; q < 4; ++q)
+              if (n + q < p.n) y[q] = f32_to_bf16_rne(o[q]);
           }
         } else {
           float *y = static_cast<float *>(p.Y) + at;
-          if (vec && n + 8 <= p.n) {
-            reinterpret_cast<float4 *>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (vec && n + 4 <= p.n) {
+            *reinterpret_cast<float4 *>(y) = v;
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (n + q < p.n) y[q] = v[q];
+            for (int q = 0; q < 4; ++q)
+              if (n + q < p.n) y[q] = o[q];
           }
         }
       }
@@ -642,7 +642,11 @@ int fp8_gemm(const Fp8Params &p, cudaStream_t st) {
   const int64_t toks = (p.m + kTok - 1) / kTok;
   const int64_t kb = (p.k + kBlk - 1) / kBlk;
   const int64_t wide = (p.n + 255) / 256 * toks;
-  if (wide >= sms) return launch_gemm<256>(p, 1, st);
+  // 256 columns where one CTA per SM fills more than half of the GPU (6144 x 4096, 700
+  // tokens: 29 us, and 54 us with 128 columns when this was chosen); else 128, two
+  // CTAs per SM, and k split while they fit (300 x 14336, 1000 tokens: 28 us, 41 us
+  // with 256 columns)
+  if (2 * wide > sms) return launch_gemm<256>(p, 1, st);
   const int64_t tiles = (p.n + 127) / 128 * toks;
   int C = 1;
   while (C < kMaxC && tiles * C * 2 <= 2 * sms && kb >= 4 * C) C *= 2;
