@@ -52,6 +52,65 @@ PyObject *pair(at::Tensor a, at::Tensor b) {
   return r;
 }
 
+// A weight or a cache comes as its tensors and is read anew on every call: a
+// tensor keeps its identity when its storage is replaced (Tensor.data, a module
+// that is moved).
+
+// (q, scale, n, k) of an Fp8Matrix
+bool matrix_of(PyObject *o, int64_t index, hyb_fp8_matrix &A) {
+  if (!PyTuple_CheckExact(o) || PyTuple_GET_SIZE(o) != 4) return false;
+  const at::Tensor *q = tensor_of(PyTuple_GET_ITEM(o, 0), index);
+  const at::Tensor *s = tensor_of(PyTuple_GET_ITEM(o, 1), index);
+  if (!q || !s || !int_of(PyTuple_GET_ITEM(o, 2), A.n) || !int_of(PyTuple_GET_ITEM(o, 3), A.k) ||
+      A.n < 1 || A.k < 1 || A.n > INT32_MAX || A.k > INT32_MAX)
+    return false;
+  const int64_t nb = up(A.n, 128) / 128, kb = up(A.k, 128) / 128;
+  if ((q->scalar_type() != at::kFloat8_e4m3fn && q->scalar_type() != at::kByte) || q->dim() != 2 ||
+      q->size(0) != A.n || q->size(1) != A.k || (A.k > 1 && q->stride(1) != 1) ||
+      (A.n > 1 && q->stride(0) < A.k))
+    return false;
+  if (s->scalar_type() != at::kFloat || s->dim() != 2 || s->size(0) != nb || s->size(1) != kb ||
+      (kb > 1 && s->stride(1) != 1) || (nb > 1 && s->stride(0) < kb))
+    return false;
+  A.q = (const uint8_t *)q->const_data_ptr();
+  A.ldq = A.n > 1 ? q->stride(0) : up(A.k, 16);
+  A.scale = s->const_data_ptr<float>();
+  A.lds = std::max(s->stride(0), kb);
+  return true;
+}
+
+// (k, v, k_scale, v_scale) of a Cache
+bool cache_of(PyObject *o, int64_t index, hyb_cache &C) {
+  if (!PyTuple_CheckExact(o) || PyTuple_GET_SIZE(o) != 4) return false;
+  const at::Tensor *t[4];
+  for (int i = 0; i < 4; ++i)
+    if (!(t[i] = tensor_of(PyTuple_GET_ITEM(o, i), index))) return false;
+  const at::Tensor &k = *t[0], &v = *t[1];
+  const bool i8 = k.scalar_type() == at::kChar;
+  if ((!i8 && k.scalar_type() != at::kFloat8_e4m3fn) || v.scalar_type() != k.scalar_type() ||
+      k.dim() != 4 || v.sizes() != k.sizes() || v.strides() != k.strides() || k.stride(3) != 1)
+    return false;
+  for (int i = 2; i < 4; ++i)
+    if (t[i]->scalar_type() != at::kFloat || t[i]->sizes() != k.sizes().slice(0, 2) ||
+        !t[i]->is_contiguous())
+      return false;
+  for (int64_t n : k.sizes())
+    if (n > INT32_MAX) return false;
+  C.k = (uint8_t *)k.data_ptr();
+  C.v = (uint8_t *)v.data_ptr();
+  C.k_scale = t[2]->data_ptr<float>();
+  C.v_scale = t[3]->data_ptr<float>();
+  C.type = i8 ? HYB_I8 : HYB_E4M3;
+  C.num_pages = (int32_t)k.size(0);
+  C.kv_heads = (int32_t)k.size(1);
+  C.page_size = (int32_t)k.size(2);
+  C.head_dim = (int32_t)k.size(3);
+  C.stride_page = k.stride(0);
+  C.stride_head = k.stride(1);
+  C.stride_token = k.stride(2);
+  return true;
+}
+
 // bf16 [rows][heads][dim] rows with dim contiguous; a single row's or head's
 // stride says nothing
 struct Rows {
@@ -130,12 +189,13 @@ PyObject *quant_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (address of the hyb_fp8_matrix, its device, X, xs, Y, ydt, flags, ws)
+// (an Fp8Matrix's tensors and sizes, its device, X, xs, Y, ydt, flags, ws)
 PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  int64_t at_, index, ydt, flags;
-  if (n != 8 || !int_of(a[0], at_) || !int_of(a[1], index) || !current(index)) Py_RETURN_NONE;
-  const hyb_fp8_matrix *A = (const hyb_fp8_matrix *)at_;
+  int64_t index, ydt, flags;
+  hyb_fp8_matrix w;
+  if (n != 8 || !int_of(a[1], index) || !current(index) || !matrix_of(a[0], index, w)) Py_RETURN_NONE;
+  const hyb_fp8_matrix *A = &w;
   const at::Tensor *X = tensor_of(a[2], index), *ws = tensor_of(a[7], index);
   if (!X || !ws || X->dim() != 2 || X->size(1) != A->k || X->size(0) < 1 ||
       (A->k > 1 && X->stride(1) != 1) || !int_of(a[5], ydt) || !int_of(a[6], flags) ||
@@ -178,12 +238,13 @@ PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (address of the hyb_cache, its device, K, V, page_table, lens, off, max_new, ws) -> True
+// (a Cache's tensors, its device, K, V, page_table, lens, off, max_new, ws) -> True
 PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  int64_t at_, index;
-  if (n != 9 || !int_of(a[0], at_) || !int_of(a[1], index) || !current(index)) Py_RETURN_NONE;
-  const hyb_cache *C = (const hyb_cache *)at_;
+  int64_t index;
+  hyb_cache cache;
+  if (n != 9 || !int_of(a[1], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
+  const hyb_cache *C = &cache;
   const at::Tensor *K = tensor_of(a[2], index), *V = tensor_of(a[3], index), *ws = tensor_of(a[8], index);
   Rows k, v;
   hyb_sequences s;
@@ -201,13 +262,14 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (address of the hyb_cache, its device, Q, page_table, lens, off, max_new, scale,
+// (a Cache's tensors, its device, Q, page_table, lens, off, max_new, scale,
 // window, sinks, out, return_lse, ws)
 PyObject *cache_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  int64_t at_, index, window, sinks;
-  if (n != 13 || !int_of(a[0], at_) || !int_of(a[1], index) || !current(index)) Py_RETURN_NONE;
-  const hyb_cache *C = (const hyb_cache *)at_;
+  int64_t index, window, sinks;
+  hyb_cache cache;
+  if (n != 13 || !int_of(a[1], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
+  const hyb_cache *C = &cache;
   const at::Tensor *Q = tensor_of(a[2], index), *ws = tensor_of(a[12], index);
   Rows q, o;
   hyb_sequences s;

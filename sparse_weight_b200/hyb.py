@@ -734,39 +734,42 @@ def _load_native():
 
 @dataclass(frozen=True)
 class Fp8Matrix:
-    """An e4m3 weight with one fp32 scale per 128 x 128 block, on the device."""
+    """An e4m3 weight with one fp32 scale per 128 x 128 block, on the device.
+    (Moving or cloning q packs its rows: where k is no multiple of 16 the copy
+    has to be given padded rows again.)"""
     n: int
     k: int
     q: torch.Tensor      # float8_e4m3fn [n][k], rows a multiple of 16 bytes apart
     scale: torch.Tensor  # fp32 [ceil(n / 128)][ceil(k / 128)]
 
     def __post_init__(self):
-        f = "Fp8Matrix"
-        _want(f, self.q.dtype in (torch.float8_e4m3fn, torch.uint8), "q must be float8_e4m3fn")
-        _want(f, self.scale.dtype == torch.float32, "scale must be fp32")
-        _want(f, tuple(self.q.shape) == (self.n, self.k), "q must be [n][k]")
-        _want(f, tuple(self.scale.shape) == (-(-self.n // 128), -(-self.k // 128)),
-              "scale must be [ceil(n / 128)][ceil(k / 128)]")
-        _want(f, (self.k == 1 or self.q.stride(1) == 1)
-              and (self.scale.shape[1] == 1 or self.scale.stride(1) == 1),
-              "rows of q and scale must be contiguous")
-        _want(f, (self.n == 1 or self.q.stride(0) >= self.k)
-              and (self.scale.shape[0] == 1 or self.scale.stride(0) >= self.scale.shape[1]),
-              "rows of q and scale must not overlap (an expanded tensor has to be copied)")
-        # the C struct, made once: the fields cannot be assigned again
-        # (a single row's stride says nothing: at least the row's length)
-        kb = self.scale.shape[1]
-        object.__setattr__(self, "_struct", HybFp8Matrix(
-            self.n, self.k, self.q.data_ptr(),
-            self.q.stride(0) if self.n > 1 else -(-self.k // 16) * 16,
-            self.scale.data_ptr(), max(self.scale.stride(0), kb)))
-        object.__setattr__(self, "_ref", ctypes.byref(self._struct))
-        object.__setattr__(self, "_at", ctypes.addressof(self._struct))
-        object.__setattr__(self, "_index", self.q.get_device()
-                           if self.q.device == self.scale.device else -1)
+        self.struct()
 
     def struct(self) -> HybFp8Matrix:
-        return self._struct
+        """The C struct, from the tensors as they are now: a tensor keeps its
+        identity when its storage is replaced (``.data``, a module moved)."""
+        f, q, s, n, k = "Fp8Matrix", self.q, self.scale, self.n, self.k
+        nb, kb = -(-n // 128), -(-k // 128)
+        _want(f, q.dtype in (torch.float8_e4m3fn, torch.uint8), "q must be float8_e4m3fn")
+        _want(f, s.dtype == torch.float32, "scale must be fp32")
+        _want(f, q.shape == (n, k), "q must be [n][k]")
+        _want(f, s.shape == (nb, kb), "scale must be [ceil(n / 128)][ceil(k / 128)]")
+        _want(f, (k == 1 or q.stride(1) == 1) and (kb == 1 or s.stride(1) == 1),
+              "rows of q and scale must be contiguous")
+        _want(f, (n == 1 or q.stride(0) >= k) and (nb == 1 or s.stride(0) >= kb),
+              "rows of q and scale must not overlap (an expanded tensor has to be copied)")
+        # (a single row's stride says nothing: at least the row's length)
+        return HybFp8Matrix(n, k, q.data_ptr(), q.stride(0) if n > 1 else -(-k // 16) * 16,
+                            s.data_ptr(), max(s.stride(0), kb))
+
+    # what the C++ binding reads, on every call anew
+    @property
+    def _at(self):
+        return self.q, self.scale, self.n, self.k
+
+    @property
+    def _index(self) -> int:
+        return self.q.get_device()
 
     def nbytes(self) -> int:
         """Bytes the product streams (values + scales)."""
@@ -860,7 +863,7 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
     f = "matmul_fp8"
     if X.dim() == 1:
         X = X.view(1, -1)
-    n, k = A.n, A.k
+    n, k, a = A.n, A.k, A.struct()
     if X.dim() != 2 or X.shape[1] != k or X.shape[0] < 1:
         raise ValueError(f"{f}: X must be [m][k]")
     m = X.shape[0]
@@ -894,7 +897,7 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
         if ws is None:
             ws = new_workspace(fp8_workspace_bytes(m, n, k), X.device)
         # a single row's stride says nothing
-        rc = lib().hyb_fp8_matmul(A._ref, m, X.data_ptr(), ldx if m > 1 else -(-k // 16) * 16, xdt,
+        rc = lib().hyb_fp8_matmul(ctypes.byref(a), m, X.data_ptr(), ldx if m > 1 else -(-k // 16) * 16, xdt,
                                   sp, lds, Y.data_ptr(), Y.stride(0) if m > 1 else n, ydt, flags,
                                   ws.data_ptr(), ws.numel(), handle)
     if rc:
@@ -920,34 +923,40 @@ class Cache:
     v_scale: torch.Tensor
 
     def __post_init__(self):
-        f = "Cache"
-        _want(f, self.k.dtype in (torch.float8_e4m3fn, torch.int8) and self.v.dtype == self.k.dtype,
+        self.struct()
+
+    def struct(self) -> HybCache:
+        """The C struct, from the tensors as they are now (see Fp8Matrix.struct)."""
+        f, k, v, ks, vs = "Cache", self.k, self.v, self.k_scale, self.v_scale
+        _want(f, k.dtype in (torch.float8_e4m3fn, torch.int8) and v.dtype == k.dtype,
               "k and v must both be float8_e4m3fn or both int8")
-        _want(f, self.k.dim() == 4 and self.v.shape == self.k.shape
-              and self.v.stride() == self.k.stride() and self.k.stride(3) == 1,
+        shape, strides = k.shape, k.stride()
+        _want(f, len(shape) == 4 and v.shape == shape and v.stride() == strides
+              and strides[3] == 1,
               "k and v must be [pages][heads][tokens][dim] of the same strides, dim contiguous")
-        _want(f, all(s.dtype == torch.float32 and s.shape == self.k.shape[:2] and s.is_contiguous()
-                     for s in (self.k_scale, self.v_scale)),
+        pages, heads, size, dim = shape
+        sp, sh, st, _ = strides
+        _want(f, ks.dtype == vs.dtype == torch.float32 and ks.shape == vs.shape == (pages, heads)
+              and ks.is_contiguous() and vs.is_contiguous(),
               "scales must be contiguous fp32 [pages][heads]")
-        _want(f, all(x.device == self.k.device for x in (self.v, self.k_scale, self.v_scale)),
+        _want(f, k.get_device() == v.get_device() == ks.get_device() == vs.get_device(),
               "all tensors must live on one device")
-        # the C struct, made once: the fields cannot be assigned again
-        pages, heads, size, dim = self.k.shape
-        sp, sh, st, _ = self.k.stride()
-        object.__setattr__(self, "_struct", HybCache(
-            self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
-            self.v_scale.data_ptr(), HYB_I8 if self.k.dtype == torch.int8 else HYB_E4M3, pages,
-            heads, size, dim, sp, sh, st))
-        object.__setattr__(self, "_ref", ctypes.byref(self._struct))
-        object.__setattr__(self, "_at", ctypes.addressof(self._struct))
-        object.__setattr__(self, "_index", self.k.get_device())
+        return HybCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                        HYB_I8 if k.dtype == torch.int8 else HYB_E4M3, pages, heads, size, dim,
+                        sp, sh, st)
+
+    # what the C++ binding reads, on every call anew
+    @property
+    def _at(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+    @property
+    def _index(self) -> int:
+        return self.k.get_device()
 
     @property
     def page_size(self) -> int:
         return self.k.shape[2]
-
-    def struct(self) -> HybCache:
-        return self._struct
 
 
 def new_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
@@ -1017,7 +1026,7 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
                 raise HybError("hyb_cache_append", r)
             return
     f = "cache_append"
-    c = C._struct
+    c = C.struct()
     heads, dim = c.kv_heads, c.head_dim
     rows, _, ldk, hsk = _heads(f, K, heads, dim, "K")
     rows_v, _, ldv, hsv = _heads(f, V, heads, dim, "V")
@@ -1031,7 +1040,7 @@ def cache_append(C: Cache, K: torch.Tensor, V: torch.Tensor, page_table: torch.T
     with scope:
         if ws is None:
             ws = new_workspace(cache_append_workspace_bytes(), C.k.device)
-        rc = lib().hyb_cache_append(C._ref, ctypes.byref(seq), K.data_ptr(), ldk, hsk,
+        rc = lib().hyb_cache_append(ctypes.byref(c), ctypes.byref(seq), K.data_ptr(), ldk, hsk,
                                     V.data_ptr(), ldv, hsv, ws.data_ptr(), ws.numel(), handle)
     if rc:
         raise HybError("hyb_cache_append", rc)
@@ -1067,7 +1076,7 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
                 raise HybError("hyb_cache_attention", r)
             return r
     f = "cache_attention"
-    c = C._struct
+    c = C.struct()
     dim = c.head_dim
     rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
     seq = _sequences(f, rows, page_table, lens, off, max_new)
@@ -1092,7 +1101,7 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
                 ws = new_workspace(cache_attention_workspace_bytes(
                     C, seq.batch, heads, seq.max_new, seq.max_pages * c.page_size), dev)
             rc = lib().hyb_cache_attention(
-                C._ref, ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso,
+                ctypes.byref(c), ctypes.byref(seq), Q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso,
                 lse.data_ptr() if return_lse else None, heads, heads,
                 dim ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),
                 handle)
