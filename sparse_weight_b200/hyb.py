@@ -716,6 +716,13 @@ def _want(fn, ok, what):
         raise ValueError(f"{fn}: {what}")
 
 
+def _int32(fn, **values):
+    """Refuse what a 32-bit field would cut off without a word."""
+    for name, v in values.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{fn}: {name} = {v} does not fit 32 bits")
+
+
 _native = None
 
 
@@ -884,6 +891,8 @@ def matmul_fp8(A: Fp8Matrix, X: torch.Tensor, xs: torch.Tensor = None, Y: torch.
         if lds < kb:
             raise ValueError(f"{f}: rows of xs must not overlap "
                              "(an expanded tensor has to be copied)")
+    if not 0 <= flags < 1 << 32:
+        raise ValueError(f"{f}: flags = {flags} does not fit 32 bits")
     ytype = _OUT_TYPES.get(ydt)
     if ytype is None:
         raise ValueError(f"{f}: ydt must be HYB_F32 or HYB_BF16")
@@ -936,6 +945,7 @@ class Cache:
               "k and v must be [pages][heads][tokens][dim] of the same strides, dim contiguous")
         pages, heads, size, dim = shape
         sp, sh, st, _ = strides
+        _int32(f, pages=pages, heads=heads, tokens=size, dim=dim)
         _want(f, ks.dtype == vs.dtype == torch.float32 and ks.shape == vs.shape == (pages, heads)
               and ks.is_contiguous() and vs.is_contiguous(),
               "scales must be contiguous fp32 [pages][heads]")
@@ -994,6 +1004,7 @@ def _sequences(f, rows, page_table, lens, off, max_new):
         if max_new is None:
             raise ValueError(f"{f}: off needs max_new")
         at = off.data_ptr()
+    _int32(f, batch=batch, max_new=max_new, pages=pages)
     return HybSequences(batch, max_new, rows, lens.data_ptr(), at, page_table.data_ptr(), pages,
                         stride)
 
@@ -1051,8 +1062,9 @@ def cache_attention_workspace_bytes(C: Cache, batch: int, heads: int, max_new: i
     """For sequences of up to max_len tokens (the page table's width times the
     page size) and max_new new ones."""
     c = C.struct()
-    n = int(lib().hyb_cache_attention_workspace_bytes(
-        ctypes.byref(c), batch, max_new, -(-max_len // C.page_size), heads))
+    pages = -(-max_len // c.page_size)
+    _int32("cache_attention_workspace_bytes", batch=batch, max_new=max_new, pages=pages, heads=heads)
+    n = int(lib().hyb_cache_attention_workspace_bytes(ctypes.byref(c), batch, max_new, pages, heads))
     if n == 0:
         raise HybError("hyb_cache_attention_workspace_bytes", HYB_ERR_INVALID_ARG)
     return n
@@ -1079,6 +1091,7 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     c = C.struct()
     dim = c.head_dim
     rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
+    _int32(f, heads=heads, window=window, sinks=sinks)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
     index = _device_of(f, C.k, Q, page_table, lens, off, out, ws)
     if out is not None:
