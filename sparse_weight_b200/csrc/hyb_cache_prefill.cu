@@ -585,28 +585,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_get(tl + kT + 32 * c, y);
         tmem_got(y);
       }
-      if (!live) continue;
-      // a row without a visible token: its products may be of anything
+      if (live) {
+        // a row without a visible token: its products may be of anything
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!some) y[e] = 0;
-      if (alone) {
-        uint16_t *to = p.O + (row0 + i) * p.ldo + hd * p.hso + 32 * c;
+        for (int e = 0; e < 32; ++e)
+          if (!some) y[e] = 0;
+        if (alone) {
+          uint16_t *to = p.O + (row0 + i) * p.ldo + hd * p.hso + 32 * c;
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t o[4];
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t o[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            o[q] = f32_to_bf16_rne(__uint_as_float(y[e + 2 * q]) * inv) |
-                   ((uint32_t)f32_to_bf16_rne(__uint_as_float(y[e + 2 * q + 1]) * inv) << 16);
-          *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int q = 0; q < 4; ++q)
+              o[q] = f32_to_bf16_rne(__uint_as_float(y[e + 2 * q]) * inv) |
+                     ((uint32_t)f32_to_bf16_rne(__uint_as_float(y[e + 2 * q + 1]) * inv) << 16);
+            *reinterpret_cast<uint4 *>(to + e) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4 *>(mypart + row * D + 32 * c + e) =
+                make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<uint4 *>(mypart + row * D + 32 * c + e) =
-              make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
       }
+      __syncwarp();  // the next read of tensor memory is the whole warp's
     }
     if (live) {
       if (!alone) {
