@@ -470,7 +470,10 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
       const int slot = j % NS;
       const uint32_t kb = ring32 + slot * (2 * kBox), vb = kb + kBox;
       const int base = base_of(j);
-      if (!mbar_wait(&full[ring_no][slot], (uint32_t)(j / NS) & 1u)) {
+      // (the vote makes the lanes one warp again for the collective instructions
+      // below, and lets none go on where another's wait ran out)
+      const bool here = mbar_wait(&full[ring_no][slot], (uint32_t)(j / NS) & 1u);
+      if (!__all_sync(0xFFFFFFFFu, here)) {
         if (lane == 0) atomicOr(p.status, kStatusTimeout);
         // the copies behind it may still land
         for (int q = j + 1; q < min(j + NS, mine); ++q)
