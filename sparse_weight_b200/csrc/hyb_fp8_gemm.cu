@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(Shape<BN>::kThreads)
   } else if (warp == 1) {
     if (lane == 0) {
       bool ok = true;
+      // X is not there before that; a bounded wait must not count the time of the
+      // kernel before this one
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int j = 0; j < nb && ok; ++j) {
         const int s = j % NS, buf = j & 1;
         ok = ring_wait(&full[s], (uint32_t)(j / NS) & 1u) &&
@@ -484,6 +487,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   } else if (warp == 1) {
     if (lane == 0) {
       bool ok = true;
+      // X is not there before that; a bounded wait must not count the time of the
+      // kernel before this one
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int j = 0; j < nb && ok; ++j) {
         const int s = j % NS, buf = j & 1;
         ok = ring_wait(&full[s], (uint32_t)(j / NS) & 1u) &&
