@@ -44,20 +44,22 @@ constexpr int kSc = 3;   // steps whose scales are held
 // 2^-28 of the largest P
 constexpr float kLift = 4.0f, kGrow = 11.0f;
 
+constexpr int kTmem = 512;
+
 template <int D>
 struct PShape {
   static constexpr int kQ = 128 * D * 2;    // a row tile's Q
   static constexpr int kOp = kT * D * 2;    // a step's K (or V) in fp16
   static constexpr int kBytes8 = kT * D;    // and in 8 bits
   static constexpr int kQOff = 0, kOpOff = 2 * kQ, kRawOff = kOpOff + kOps * kOp;
-  static constexpr int kBytes = kRawOff + kRaw * kBytes8;
+  // (at 64 dimensions more than is used: the SM's tensor memory is this CTA's alone)
+  static constexpr int kUsed = kRawOff + kRaw * kBytes8;
+  static constexpr int kBytes = kUsed > kSmemPerSm / 3 * 2 ? kUsed : kSmemPerSm / 3 * 2 + 1024;
   static constexpr int kTile = kT + D;      // tensor-memory columns of a row tile
   static constexpr int kPart = kPrefillRows * D + 2 * kPrefillRows;
-  static_assert(2 * kTile <= 512, "tensor memory");
+  static_assert(2 * kTile <= kTmem, "tensor memory");
+  static_assert(tmem_fits(kTmem, kBytes), "tensor memory of the CTAs that fit an SM");
 };
-constexpr int kTmem = 512;
-// (With its 512 threads of 121 to 128 registers a CTA has its SM to itself: none of
-// a kernel that starts early, with tensor memory of its own, can be beside it.)
 
 // The MMA warp runs as a whole and only its leader's instructions take effect:
 // operands then stay in uniform registers (from a branch of one lane they were

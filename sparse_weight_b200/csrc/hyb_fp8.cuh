@@ -62,12 +62,8 @@ struct Fp8Params {
 // reads of W where early_w allows them.  Every CTA waits, so that a kernel's end
 // also means the end of all before it.
 //
-// The tensor-core kernels allocate tensor memory before that wait.  A CTA that
-// holds some while it waits must not keep it from a CTA of the kernel it waits for:
-// those that can share an SM never need more than its 512 columns together.  By
-// shared memory two of at most 256 columns fit an SM, or one of 512; a prefill
-// attention CTA, which needs 512, takes all of the SM's registers.
-constexpr int kSmemPerSm = 228 << 10;
+// The tensor-core kernels allocate tensor memory before that wait: see
+// hyb_tcgen05.cuh.
 
 // The tensor-core product (hyb_fp8_gemm.cu) of e4m3 operands.
 int fp8_gemm(const Fp8Params &p, cudaStream_t st);

@@ -52,8 +52,7 @@ struct Shape {
   static constexpr int kCtl = 2;
   static constexpr int kThreads = 32 * (kCtl + 8);
   static_assert(kTok * kPitch * 4 <= kRing, "the result reuses the ring");
-  static_assert(kRing > (kTmem <= 256 ? kSmemPerSm / 3 : kSmemPerSm * 2 / 3),
-                "tensor memory of the CTAs that fit an SM");
+  static_assert(tmem_fits(kTmem, kRing), "tensor memory of the CTAs that fit an SM");
   static_assert(kStage % 1024 == 0, "swizzle alignment");
 };
 
@@ -412,7 +411,7 @@ struct DecodeShape {
   static constexpr int kTmem = 2 * BN;
   static constexpr int kLoad = 16;
   static_assert(kDecodeTokens * kPitch * 4 <= kStage * kStages, "the result reuses the ring");
-  static_assert(kTmem <= 256 && kBytes > kSmemPerSm / 3, "tensor memory of the CTAs that fit an SM");
+  static_assert(tmem_fits(kTmem, kBytes), "tensor memory of the CTAs that fit an SM");
   static_assert(kStage % 1024 == 0, "swizzle alignment");
 };
 

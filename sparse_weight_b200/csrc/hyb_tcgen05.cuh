@@ -7,6 +7,17 @@
 
 namespace hyb {
 
+// Tensor memory of kernels that are programmatic dependents and allocate it before
+// griddepcontrol.wait.  A CTA that holds some while it waits must not keep it from a
+// CTA of the kernel it waits for: those that can share an SM never need more than its
+// 512 columns together.  Shared memory sees to that, asserted beside each kernel: a
+// CTA takes more than a third of an SM's for up to 256 columns, so that two fit an SM,
+// and more than two thirds for 512, so that no other fits beside it.
+constexpr int kSmemPerSm = 228 << 10;
+constexpr bool tmem_fits(int columns, int smem) {
+  return smem > (columns <= 256 ? kSmemPerSm / 3 : kSmemPerSm / 3 * 2);
+}
+
 // Shared-memory matrix descriptor of a K-major operand in the 128-byte
 // swizzle layout: rows 128 bytes apart, 8-row groups 1024 bytes apart
 // (stride byte offset), descriptor version 1, layout type 2 (128B swizzle).
