@@ -80,7 +80,11 @@ class AttentionBlock:
         lens their lengths with them (see hyb.cache_append); max_new is the most
         of one sequence (by default rows / batch, with off the block's).  ``rotate(q, k)``
         may return position-dependent q [rows][heads][dim] and k
-        [rows][kv_heads][dim].  Returns bf16 [rows][wo.n]."""
+        [rows][kv_heads][dim].  Returns bf16 [rows][wo.n].
+
+        With off, rows behind the last sequence (off[batch] .. rows - 1: a step of
+        a fixed size that is not full) get the output of a zero attention.  x is
+        multiplied there too: keep it finite, as elsewhere."""
         rows = x.shape[0]
         batch, pages = page_table.shape
         if max_new is not None:
@@ -91,6 +95,8 @@ class AttentionBlock:
                 or new > self.max_new:
             raise ValueError("AttentionBlock: the step is larger than the block was made for")
         kv_heads, dim = self.cache.k.shape[1], self.cache.k.shape[3]
+        # the attention leaves rows of no sequence as they were, and the last product reads them
+        a = None if off is None else torch.zeros(rows, self.heads, dim, dtype=torch.bfloat16, device=x.device)
         xq = xs = None
         if rows > 16 and sum(isinstance(w, hyb.Fp8Matrix) for w in (self.wq, self.wk, self.wv)) > 1:
             xq, xs = hyb.quant_fp8(x, ws=self._ws_quant)  # once for the products that share x
@@ -101,7 +107,7 @@ class AttentionBlock:
             q, k = rotate(q, k)
         hyb.cache_append(self.cache, k, v, page_table, lens, off, new, ws=self._ws_append)
         a = hyb.cache_attention(self.cache, q, page_table, lens, off, new, window=self.window,
-                                sinks=self.sinks, ws=self._ws_attention)
+                                sinks=self.sinks, out=a, ws=self._ws_attention)
         return self._product(self.wo, a.view(rows, self.heads * dim))
 
     def check(self) -> None:
