@@ -751,6 +751,8 @@ class Fp8Matrix:
 
     def __post_init__(self):
         self.struct()
+        # what the C++ binding reads, on every call anew
+        object.__setattr__(self, "_at", (self.q, self.scale, self.n, self.k))
 
     def struct(self) -> HybFp8Matrix:
         """The C struct, from the tensors as they are now: a tensor keeps its
@@ -768,11 +770,6 @@ class Fp8Matrix:
         # (a single row's stride says nothing: at least the row's length)
         return HybFp8Matrix(n, k, q.data_ptr(), q.stride(0) if n > 1 else -(-k // 16) * 16,
                             s.data_ptr(), max(s.stride(0), kb))
-
-    # what the C++ binding reads, on every call anew
-    @property
-    def _at(self):
-        return self.q, self.scale, self.n, self.k
 
     @property
     def _index(self) -> int:
@@ -933,6 +930,8 @@ class Cache:
 
     def __post_init__(self):
         self.struct()
+        # what the C++ binding reads, on every call anew
+        object.__setattr__(self, "_at", (self.k, self.v, self.k_scale, self.v_scale))
 
     def struct(self) -> HybCache:
         """The C struct, from the tensors as they are now (see Fp8Matrix.struct)."""
@@ -954,11 +953,6 @@ class Cache:
         return HybCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
                         HYB_I8 if k.dtype == torch.int8 else HYB_E4M3, pages, heads, size, dim,
                         sp, sh, st)
-
-    # what the C++ binding reads, on every call anew
-    @property
-    def _at(self):
-        return self.k, self.v, self.k_scale, self.v_scale
 
     @property
     def _index(self) -> int:

@@ -85,6 +85,7 @@ def test_copies():
                 a, b = getattr(X, w), getattr(Y, w)
                 assert getattr(s, w) == b.data_ptr() != a.data_ptr() and a.dtype == b.dtype
                 assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+                assert any(t is b for t in Y._at)  # the C++ binding's view of it, too
 
 
 def value(A, x):
