@@ -456,7 +456,9 @@ HYB_API int hyb_fp8_matmul(const hyb_fp8_matrix *A, int64_t m, const void *X, in
  * place, d) is at page * stride_page + head * stride_head +
  * place * stride_token + d of k (and of v); scale (page, head) at
  * page * kv_heads + head of k_scale (v_scale).  Strides in bytes, positive
- * multiples of 16; any order of the axes. */
+ * multiples of 16; any order of the axes.  Scales are finite and not negative,
+ * V's 2^120 at most (hyb_cache_append writes 2^-40 to 2^60); what the attention
+ * gives for rows that see others is unspecified. */
 typedef struct {
   uint8_t *k, *v;            /* 16-byte aligned */
   float *k_scale, *v_scale;  /* [num_pages][kv_heads] */
@@ -472,7 +474,9 @@ typedef struct {
  * lie one sequence after another in the rows of K, V (hyb_cache_append) and Q,
  * O (hyb_cache_attention): sequence b's are rows off[b] .. off[b + 1] - 1, or,
  * with off NULL, rows b * max_new .. + max_new - 1 (every sequence has max_new
- * of them).  An empty slot has lens[b] == 0: its rows are ignored by the
+ * of them).  Rows behind the last sequence (off[batch] .. rows - 1) belong to
+ * none: what is there is not read, and those of O and lse are left as they
+ * were.  An empty slot has lens[b] == 0: its rows are ignored by the
  * append and get the empty row's result from the attention.  Device data are
  * checked on the device: a page outside 0 .. num_pages - 1, a length below 0
  * or above max_pages * page_size, fewer tokens than new ones (unless 0), off
@@ -537,8 +541,12 @@ HYB_API size_t hyb_cache_attention_workspace_bytes(const hyb_cache *C, int32_t b
  *      softmax's sum of exponentials, or NULL
  * heads is a multiple of kv_heads; window >= 0 (0 = none), sinks >= 0.
  * fp32 accumulation and softmax statistics; the probabilities are rounded to
- * 11 bits for the second product.  Value scales below 2^-64, 0 among them, count
- * as 2^-64 there.  A cached NaN counts where a query of the sequence sees its
+ * 11 bits (fp16) for the second product, whose other operand, 8 bits, is exact
+ * in fp16.  Value scales below 2^-64, 0 among them, count as 2^-64 there.  The
+ * host does not know lens, so the work is split over the GPU for sequences as
+ * long as the page table is wide (max_pages): a table much wider than the step's
+ * longest sequence leaves SMs idle; a smaller max_pages over the same table (and
+ * table_stride) avoids that.  A cached NaN counts where a query of the sequence sees its
  * token; tokens that none sees are not used, nor are the table entries and the
  * scales of pages of which none sees a token (they need not be valid).  O must
  * not overlap Q.  Tickets and

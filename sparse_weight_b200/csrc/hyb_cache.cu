@@ -59,7 +59,8 @@ __device__ __forceinline__ float2 unpack2(uint32_t two) {
 // tokens do not wait for the page table; the largest value is found in the bits,
 // two at a time; and where the scale is a power of two (always, unless the page
 // brought another one) its reciprocal is exact and the divisions are products.
-// 3 prompts of up to 2048 tokens (8 heads of 128, 8-bit integers): 6.0 us, was 14.5 (64 x 1 token: 3.4, was 6.1).
+// 3 prompts of up to 2048 tokens (8 heads of 128, 8-bit integers): 5.8 us in a graph, 7.4
+// with inputs that are not in L2 (floor 3.4); 64 x 1 token: 3.3 us, a chain of latencies.
 template <int D, bool I8>
 __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p) {
   constexpr int LANES = D / 8;         // threads per token
@@ -176,7 +177,11 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams p)
 
 constexpr int kStep = 32;   // tokens per step
 constexpr int kWarps = 4;   // warps that compute
-// Probabilities are held times 2^4 where the reference of the exponentials is the
+// Probabilities are rounded to fp16 for the second product: the tensor cores take 16
+// bits, V's 8-bit values are exact in fp16, and bf16 would keep 8 bits of P instead
+// of 11.  (The sum of the softmax is of the fp32 ones.  The error against 64 bits is
+// 0.0016 to 0.0017 of the output's size with it and without it: bf16's rounding of O.)
+// They are held times 2^4 where the reference of the exponentials is the
 // largest exponent, and times 2^15 at most: the reference moves only where it has
 // been outgrown by more (a vote instead of a maximum over lanes in most steps).
 // fp16's smallest step is then at most 2^-28 of the largest probability.
@@ -238,7 +243,11 @@ struct AttnShape {
 //
 // Bound by the latency of a warp's chain (a third of the issue slots are used, the
 // tensor pipe a sixth): 32 sequences to 8192, 64 heads over 8: 44.7 us, 4.4 TB/s;
-// 8 x 4 tokens in a window of 4096, 32 heads over 8: 24.8 us.  Measured and not kept:
+// 8 x 4 tokens in a window of 4096, 32 heads over 8: 25.3 us (2.8 times the floor).
+// Split rows, 8 x 4 tokens over 8192, 64 heads over 8 (32 rows a unit): 150 us (0.9 TB/s),
+// 100 us at 64 dimensions; a quarter of the issue slots are used.  At 128 dimensions 88 to
+// 92 bytes are spilled: 10 warps on an SM put three on one scheduler (168 registers).
+// Measured and not kept:
 // 3 CTAs per SM for 16 rows (28 to 31 us for the latter), units' first parts before
 // all second ones (48 us for the former).
 template <int D, bool I8, int NR, bool SHARE>
@@ -784,9 +793,17 @@ int seq_check(const hyb_cache *C, const hyb_sequences *S, SeqParams *p) {
 // units alone fill the GPU, and there for units of few rows only, a CTA has at
 // most 40 steps (else 64), so that sequences of different lengths end at about
 // the same time: 32 sequences of 1024 to 8192 tokens took 49.6 us with 48 steps
-// and 46.9 us with 32, one of 65536 45 us with 32 and 36 us with 40.  Only units
-// that are split have tickets, which lie at a fixed place whatever the call's
-// shape, so that calls of different shapes can share a workspace.
+// and 46.9 us with 32, one of 65536 45 us with 32 and 36 us with 40.  (12, 40, and 3
+// CTAs instead of 4 rest on those cases; sizes beside them were not measured.)
+//
+// The host has no lengths, so the steps are those of the table's width: 8192 tokens
+// in a table of 131072 take 22 us instead of 19 (1 token, 32 heads over 8; 13 in one
+// of 16384), 143 instead of 38 (4 tokens, 64 heads), 183 instead of 54 (64 tokens).
+// `many` units stay whole whatever their lengths: 148 sequences of 1024, one of
+// them of 65536, take 440 us, 147 take 191.
+//
+// Only units that are split have tickets, which lie at a fixed place whatever the
+// call's shape, so that calls of different shapes can share a workspace.
 constexpr int kMinChunk = 4, kUnsplit = 12;
 constexpr int kShareRows = 64;  // most rows of mma.sync units
 constexpr int kTickets = 2048;

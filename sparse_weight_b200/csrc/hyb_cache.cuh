@@ -50,7 +50,7 @@ struct AttnParams {
   int window, sinks;
   int qtiles;  // units per sequence and head
   int splits, chunk;  // CTAs per unit, steps of each
-  float *part;        // [unit][split]: O [16][D], mref [16], l [16]
+  float *part;        // [unit][split]: O [rows][D], reference [rows], sum [rows], rows of a unit
   uint32_t *tickets;  // [unit]
   uint32_t *status;
 };

@@ -20,11 +20,16 @@
 //     partial sums meet in distributed shared memory in a fixed order.
 //
 // Bound by the epilogue's reads of tensor memory and FMAs beside the MMAs.  2048
-// tokens x 14336 x 4096: 168 us (1.43 PFLOP/s) with BN = 256, the quantiser
-// included (BN = 224, whose 6.9 rounds of CTAs waste less than 6.05, 176 us; rows of W
-// first, 171 us, W read three times); 45 x 1000 x 4100 in e4m3: 6.9 us, latency;
-// 128 x 4096 x 4096 in bf16: 15 us, and 33 us when the lanes that add up a cluster's
-// sums read 32 bytes apart from one another.
+// tokens x 14336 x 4096: 178 us (1.35 PFLOP/s) with BN = 256, the quantiser
+// included, of which a seventh round of 8 tiles takes a whole tile's time; 45 x 1000 x
+// 4100 in e4m3: 7.5 us, latency of one launch whose 64 CTAs leave half of the SMs idle;
+// 128 x 4096 x 4096 in bf16: 15.9 us.  With inputs in L2 these take 168, 6.8 and 14.9
+// us, and so measured the first took 176 us with BN = 224 (6.9 rounds of CTAs), 171 with
+// rows of W first (W read three times), and the last 33 us when the lanes that add up
+// a cluster's sums read 32 bytes apart from one another.
+//
+// Registers: 12 bytes are spilled at BN = 128 (two CTAs per SM), 32 at BN = 256, whose
+// 10 warps put three on a scheduler (168 registers).
 #include "hyb_fp8.cuh"
 #include "hyb_tcgen05.cuh"
 
@@ -390,8 +395,9 @@ int launch_gemm(const Fp8Params &p, int C, cudaStream_t st) {
 // not looked at (the MMA unit has the time, and its operand rows 32 .. 127 are
 // whatever lies behind X's 4 KB: W's tile, and behind a narrow one the next
 // stage's).  Two warps, half of the columns each, scale and add.  16 x 4096 x
-// 14336: 15.7 us with the quantiser's kernel, 13.8 us (4.3 TB/s) without; W comes at
-// the copy rate while it comes, the rest is the clusters' start and last sums.  Quantising a
+// 14336: 15.8 us with the quantiser's kernel, 13.8 us (4.3 TB/s) without (13.1 and 11.4
+// where W is in L2); its 256 equal CTAs leave some SMs with two and some with one, and
+// the clusters' start and last sums come on top.  Quantising a
 // bf16 X in this kernel, by the warps that are idle, was slower than a kernel
 // before it that this one overlaps (16 x 4096 x 14336: 27 us and 16 us): every
 // row tile does that work again.
@@ -650,7 +656,7 @@ int fp8_gemm(const Fp8Params &p, cudaStream_t st) {
   // 256 columns where one CTA per SM fills more than half of the GPU (6144 x 4096, 700
   // tokens: 29 us, and 54 us with 128 columns when this was chosen); else 128, two
   // CTAs per SM, and k split while they fit (300 x 14336, 1000 tokens: 28 us, 41 us
-  // with 256 columns)
+  // with 256 columns); the border itself was not measured
   if (2 * wide > sms) return launch_gemm<256>(p, 1, st);
   const int64_t tiles = (p.n + 127) / 128 * toks;
   int C = 1;
