@@ -716,11 +716,10 @@ def _want(fn, ok, what):
         raise ValueError(f"{fn}: {what}")
 
 
-def _int32(fn, **values):
+def _int32(fn, names, *values):
     """Refuse what a 32-bit field would cut off without a word."""
-    for name, v in values.items():
-        if not -1 << 31 <= v < 1 << 31:
-            raise ValueError(f"{fn}: {name} = {v} does not fit 32 bits")
+    if min(values) < -1 << 31 or max(values) >= 1 << 31:
+        raise ValueError(f"{fn}: one of {names} = {values} does not fit 32 bits")
 
 
 _native = None
@@ -763,13 +762,14 @@ class Fp8Matrix:
         _want(f, s.dtype == torch.float32, "scale must be fp32")
         _want(f, q.shape == (n, k), "q must be [n][k]")
         _want(f, s.shape == (nb, kb), "scale must be [ceil(n / 128)][ceil(k / 128)]")
-        _want(f, (k == 1 or q.stride(1) == 1) and (kb == 1 or s.stride(1) == 1),
+        (ldq, one), (lds, sone) = q.stride(), s.stride()
+        _want(f, (k == 1 or one == 1) and (kb == 1 or sone == 1),
               "rows of q and scale must be contiguous")
-        _want(f, (n == 1 or q.stride(0) >= k) and (nb == 1 or s.stride(0) >= kb),
+        _want(f, (n == 1 or ldq >= k) and (nb == 1 or lds >= kb),
               "rows of q and scale must not overlap (an expanded tensor has to be copied)")
         # (a single row's stride says nothing: at least the row's length)
-        return HybFp8Matrix(n, k, q.data_ptr(), q.stride(0) if n > 1 else -(-k // 16) * 16,
-                            s.data_ptr(), max(s.stride(0), kb))
+        return HybFp8Matrix(n, k, q.data_ptr(), ldq if n > 1 else -(-k // 16) * 16,
+                            s.data_ptr(), max(lds, kb))
 
     @property
     def _index(self) -> int:
@@ -944,7 +944,7 @@ class Cache:
               "k and v must be [pages][heads][tokens][dim] of the same strides, dim contiguous")
         pages, heads, size, dim = shape
         sp, sh, st, _ = strides
-        _int32(f, pages=pages, heads=heads, tokens=size, dim=dim)
+        _int32(f, "pages, heads, tokens, dim", *shape)
         _want(f, ks.dtype == vs.dtype == torch.float32 and ks.shape == vs.shape == (pages, heads)
               and ks.is_contiguous() and vs.is_contiguous(),
               "scales must be contiguous fp32 [pages][heads]")
@@ -998,7 +998,7 @@ def _sequences(f, rows, page_table, lens, off, max_new):
         if max_new is None:
             raise ValueError(f"{f}: off needs max_new")
         at = off.data_ptr()
-    _int32(f, batch=batch, max_new=max_new, pages=pages)
+    _int32(f, "batch, max_new, pages", batch, max_new, pages)
     return HybSequences(batch, max_new, rows, lens.data_ptr(), at, page_table.data_ptr(), pages,
                         stride)
 
@@ -1057,7 +1057,8 @@ def cache_attention_workspace_bytes(C: Cache, batch: int, heads: int, max_new: i
     page size) and max_new new ones."""
     c = C.struct()
     pages = -(-max_len // c.page_size)
-    _int32("cache_attention_workspace_bytes", batch=batch, max_new=max_new, pages=pages, heads=heads)
+    _int32("cache_attention_workspace_bytes", "batch, max_new, pages, heads", batch, max_new, pages,
+           heads)
     n = int(lib().hyb_cache_attention_workspace_bytes(ctypes.byref(c), batch, max_new, pages, heads))
     if n == 0:
         raise HybError("hyb_cache_attention_workspace_bytes", HYB_ERR_INVALID_ARG)
@@ -1085,7 +1086,7 @@ def cache_attention(C: Cache, Q: torch.Tensor, page_table: torch.Tensor, lens: t
     c = C.struct()
     dim = c.head_dim
     rows, heads, ldq, hsq = _heads(f, Q, None, dim, "Q")
-    _int32(f, heads=heads, window=window, sinks=sinks)
+    _int32(f, "heads, window, sinks", heads, window, sinks)
     seq = _sequences(f, rows, page_table, lens, off, max_new)
     index = _device_of(f, C.k, Q, page_table, lens, off, out, ws)
     if out is not None:
