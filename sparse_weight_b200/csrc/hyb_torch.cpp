@@ -1,8 +1,8 @@
 // The 8-bit operators of hyb.py for a call that needs nothing special: plain CUDA
 // tensors on the current device and stream and a workspace at hand.  A step of a
 // decode loop makes many of these calls, and the kernels of small ones take less
-// time than the binding's Python code and ctypes do (matmul_fp8: 19 us, 3.7 through here;
-// cache_attention: 27 and 5.1).
+// time than the binding's Python code and ctypes do (matmul_fp8: 18 us, 3.4 through here;
+// cache_attention: 26 and 4.6).
 //
 // A function returns its outputs, an int where the library refused the call (the
 // status), or None where the call is not of this kind: hyb.py then goes its own
@@ -22,13 +22,25 @@ namespace {
 const at::Tensor *tensor_of(PyObject *o, int64_t index) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor &t = THPVariable_Unpack(o);
-  return t.is_cuda() && t.get_device() == index && t.layout() == at::kStrided ? &t : nullptr;
+  const at::Device d = t.device();
+  return d.is_cuda() && d.index() == index && t.layout() == at::kStrided ? &t : nullptr;
 }
 bool int_of(PyObject *o, int64_t &v) {
   if (!PyLong_CheckExact(o)) return false;
   int over = 0;
   v = PyLong_AsLongLongAndOverflow(o, &over);
   return over == 0;
+}
+// the device that a weight or a cache, given as its tensors, has to be on: `o`,
+// or with None the first tensor's
+bool index_of(PyObject *o, PyObject *tensors, int64_t &index) {
+  if (o != Py_None) return int_of(o, index);
+  if (!PyTuple_CheckExact(tensors) || PyTuple_GET_SIZE(tensors) < 1 ||
+      !THPVariable_CheckExact(PyTuple_GET_ITEM(tensors, 0)))
+    return false;
+  const at::Device d = THPVariable_Unpack(PyTuple_GET_ITEM(tensors, 0)).device();
+  index = d.is_cuda() ? d.index() : -1;
+  return true;
 }
 bool current(int64_t index) { return index >= 0 && c10::cuda::current_device() == index; }
 hyb_stream_t stream_of(int64_t index) {
@@ -190,12 +202,12 @@ PyObject *quant_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (an Fp8Matrix's tensors and sizes, its device, X, xs, Y, ydt, flags, ws)
+// (an Fp8Matrix's tensors and sizes, device or None, X, xs, Y, ydt, flags, ws)
 PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t index, ydt, flags;
   hyb_fp8_matrix w;
-  if (n != 8 || !int_of(a[1], index) || !current(index) || !matrix_of(a[0], index, w)) Py_RETURN_NONE;
+  if (n != 8 || !index_of(a[1], a[0], index) || !current(index) || !matrix_of(a[0], index, w)) Py_RETURN_NONE;
   const hyb_fp8_matrix *A = &w;
   const at::Tensor *X = tensor_of(a[2], index), *ws = tensor_of(a[7], index);
   if (!X || !ws || X->dim() != 2 || X->size(1) != A->k || X->size(0) < 1 ||
@@ -239,12 +251,12 @@ PyObject *matmul_fp8(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (a Cache's tensors, its device, K, V, page_table, lens, off, max_new, ws) -> True
+// (a Cache's tensors, device or None, K, V, page_table, lens, off, max_new, ws) -> True
 PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t index;
   hyb_cache cache;
-  if (n != 9 || !int_of(a[1], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
+  if (n != 9 || !index_of(a[1], a[0], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
   const hyb_cache *C = &cache;
   const at::Tensor *K = tensor_of(a[2], index), *V = tensor_of(a[3], index), *ws = tensor_of(a[8], index);
   Rows k, v;
@@ -263,13 +275,13 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (a Cache's tensors, its device, Q, page_table, lens, off, max_new, scale,
+// (a Cache's tensors, device or None, Q, page_table, lens, off, max_new, scale,
 // window, sinks, out, return_lse, ws)
 PyObject *cache_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   int64_t index, window, sinks;
   hyb_cache cache;
-  if (n != 13 || !int_of(a[1], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
+  if (n != 13 || !index_of(a[1], a[0], index) || !current(index) || !cache_of(a[0], index, cache)) Py_RETURN_NONE;
   const hyb_cache *C = &cache;
   const at::Tensor *Q = tensor_of(a[2], index), *ws = tensor_of(a[12], index);
   Rows q, o;

@@ -771,9 +771,7 @@ class Fp8Matrix:
         return HybFp8Matrix(n, k, q.data_ptr(), ldq if n > 1 else -(-k // 16) * 16,
                             s.data_ptr(), max(lds, kb))
 
-    @property
-    def _index(self) -> int:
-        return self.q.get_device()
+    _index = None  # (for the binding: its tensors' own device)
 
     def nbytes(self) -> int:
         """Bytes the product streams (values + scales)."""
@@ -954,9 +952,7 @@ class Cache:
                         HYB_I8 if k.dtype == torch.int8 else HYB_E4M3, pages, heads, size, dim,
                         sp, sh, st)
 
-    @property
-    def _index(self) -> int:
-        return self.k.get_device()
+    _index = None  # (for the binding: its tensors' own device)
 
     @property
     def page_size(self) -> int:
