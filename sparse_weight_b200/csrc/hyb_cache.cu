@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(AttnShape<D, NR, SHARE>::kThreads, NR == 1 ? 3
                 for (int q = 0; q < D / 32; ++q) w[e][q] = 0;
               }
             }
-            asm volatile("" ::: "memory");
+            __syncwarp();  // (the products below are the whole warp's)
           }
 #pragma unroll
           for (int q = 0; q < D / 32; ++q)
