@@ -243,7 +243,7 @@ struct AttnShape {
 //
 // Bound by the latency of a warp's chain (a third of the issue slots are used, the
 // tensor pipe a sixth): 32 sequences to 8192, 64 heads over 8: 44.7 us, 4.4 TB/s;
-// 8 x 4 tokens in a window of 4096, 32 heads over 8: 25.3 us (2.8 times the floor).
+// 8 x 4 tokens in a window of 4096, 32 heads over 8: 25.4 us (2.8 times the floor).
 // Split rows, 8 x 4 tokens over 8192, 64 heads over 8 (32 rows a unit): 150 us (0.9 TB/s),
 // 100 us at 64 dimensions; a quarter of the issue slots are used.  At 128 dimensions 88 to
 // 92 bytes are spilled: 10 warps on an SM put three on one scheduler (168 registers).

@@ -119,7 +119,7 @@ __device__ __forceinline__ uint2 to_e4m3(const Raw<F32> &r, float inv) {
 // 8 bytes written), with all of them on their way at once.  The instructions
 // count here as much as the bytes: the largest values are compared as bits, two
 // at a time, and a lane makes one of its half-warp's 2 kSeg divisions.  2048 x 14336
-// in bf16: 16.9 us a call with changing inputs, 0.80 of the measured copy rate (15.4 us
+// in bf16: 17.0 us a call with changing inputs, 0.80 of the measured copy rate (15.4 us
 // in a graph; 14.6 where the inputs are in L2).
 template <bool F32, int kSeg>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(int64_t rows, int64_t cols64,

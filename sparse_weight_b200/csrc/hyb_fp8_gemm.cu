@@ -20,7 +20,7 @@
 //     partial sums meet in distributed shared memory in a fixed order.
 //
 // Bound by the epilogue's reads of tensor memory and FMAs beside the MMAs.  2048
-// tokens x 14336 x 4096: 178 us (1.35 PFLOP/s) with BN = 256, the quantiser
+// tokens x 14336 x 4096: 180 us (1.34 PFLOP/s) with BN = 256, the quantiser
 // included, of which a seventh round of 8 tiles takes a whole tile's time; 45 x 1000 x
 // 4100 in e4m3: 7.5 us, latency of one launch whose 64 CTAs leave half of the SMs idle;
 // 128 x 4096 x 4096 in bf16: 15.9 us.  With inputs in L2 these take 168, 6.8 and 14.9
